@@ -6,6 +6,7 @@ of the computation runs in the library's CUDA kernels; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -76,6 +77,29 @@ class SkaDecodeArgs(ctypes.Structure):
                 ("k_cache", _VP), ("v_cache", _VP), ("pos", _VP), ("advance_pos", _I), ("o", _VP)]
 
 
+class SsmArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("H", _I), ("G", _I), ("T", _I), ("D", _I), ("N", _I), ("W", _I), ("dtype", _I),
+                ("gate_inputs", _I), ("conv_silu", _I), ("x", _VP), ("dt", _VP), ("Bm", _VP), ("Cm", _VP),
+                ("z", _VP), ("A", _VP), ("dt_bias", _VP), ("feedthrough", _VP), ("conv_weight", _VP),
+                ("conv_bias", _VP), ("conv_state_in", _VP), ("S0", _VP), ("lengths", _VP), ("y", _VP),
+                ("ST", _VP), ("conv_state_out", _VP), ("saved_states", _VP), ("workspace", _VP),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class SsmBwdArgs(ctypes.Structure):
+    _fields_ = [("fwd", SsmArgs), ("grad_y", _VP), ("grad_ST", _VP), ("grad_conv_state_out", _VP),
+                ("grad_x", _VP), ("grad_dt", _VP), ("grad_z", _VP), ("grad_B", _VP), ("grad_C", _VP),
+                ("grad_A", _VP), ("grad_dt_bias", _VP), ("grad_feedthrough", _VP), ("grad_conv_weight", _VP),
+                ("grad_conv_bias", _VP), ("grad_S0", _VP), ("grad_conv_state_in", _VP)]
+
+
+class SsmStepArgs(ctypes.Structure):
+    _fields_ = [("B", _I), ("H", _I), ("G", _I), ("D", _I), ("N", _I), ("W", _I), ("dtype", _I),
+                ("gate_inputs", _I), ("conv_silu", _I), ("x", _VP), ("dt", _VP), ("Bm", _VP), ("Cm", _VP),
+                ("z", _VP), ("A", _VP), ("dt_bias", _VP), ("feedthrough", _VP), ("conv_weight", _VP),
+                ("conv_bias", _VP), ("S", _VP), ("conv_state", _VP), ("y", _VP)]
+
+
 class RdmError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -89,7 +113,8 @@ EXPORTS = ["rdm_ddts_fwd", "rdm_ddts_fwd_workspace_size", "rdm_ddts_saved_states
            "rdm_ddts_sync_status",
            "rdm_status_string", "rdm_ddts_set_test_hooks", "rdm_ddts_version", "rdm_shortconv_fwd",
            "rdm_shortconv_bwd", "rdm_shortconv_fwd_many", "rdm_shortconv_bwd_many", "rdm_ska_fwd",
-           "rdm_ska_decode"]
+           "rdm_ska_decode", "rdm_ssm_fwd", "rdm_ssm_fwd_workspace_size", "rdm_ssm_saved_states_size",
+           "rdm_ssm_bwd", "rdm_ssm_bwd_workspace_size", "rdm_ssm_step"]
 
 
 def load():
@@ -132,6 +157,16 @@ def load():
         lib.rdm_ska_fwd.restype = _I
         lib.rdm_ska_decode.argtypes = [ctypes.POINTER(SkaDecodeArgs), _VP]
         lib.rdm_ska_decode.restype = _I
+        for name, args in (("rdm_ssm_fwd", SsmArgs), ("rdm_ssm_bwd", SsmBwdArgs)):
+            fn, size = getattr(lib, name), getattr(lib, name + "_workspace_size")
+            fn.argtypes = [ctypes.POINTER(args), _VP]
+            fn.restype = _I
+            size.argtypes = [ctypes.POINTER(args)]
+            size.restype = ctypes.c_size_t
+        lib.rdm_ssm_saved_states_size.argtypes = [_I] * 5
+        lib.rdm_ssm_saved_states_size.restype = ctypes.c_size_t
+        lib.rdm_ssm_step.argtypes = [ctypes.POINTER(SsmStepArgs), _VP]
+        lib.rdm_ssm_step.restype = _I
         lib.rdm_ddts_set_test_hooks.argtypes = [ctypes.c_longlong, _I]
         lib.rdm_ddts_set_test_hooks.restype = _I
         lib.rdm_ddts_version.argtypes = []
@@ -465,6 +500,223 @@ def rdm_ska_decode(q, k, v, k_cache, v_cache, pos, *, scale=0.0, advance_pos=Tru
                       _ptr(o))
     _check(load().rdm_ska_decode(ctypes.byref(a), _stream(stream)), "rdm_ska_decode")
     return o
+
+
+# ---------------------------------------------------------------- selective scan
+def _on(stream):
+    """Context in which `stream` (torch stream or handle) is the current one, so
+    that what a call allocates belongs to the stream it runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(_stream(stream)))
+
+
+def _current(t: torch.Tensor):
+    """The device of `t`, which has to be the current one: the library launches there."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the library must be contiguous CUDA tensors")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _arg(t, name, shape, dtype, device):
+    """The pointer of argument `name` (None stays None) after its checks."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to the library must be contiguous and on {device}")
+    return t.data_ptr()
+
+
+def _buffer(t, name, device):
+    """Pointer and bytes of a buffer of which only the size matters."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to the library must be contiguous and on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+_F32 = torch.float32
+
+
+def _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
+              conv_silu, lengths, gates, y, ST, conv_state_out, saved_states):
+    dev = _current(x)
+    if x.dim() != 4 or A.dim() != 3 or Bm.dim() != 4:
+        raise ValueError("x: expected [B,H,T,D], A: [H,D,N], Bm: [B,G,T,N]")
+    B, H, T, D = x.shape
+    N, G = A.shape[-1], Bm.shape[1]
+    code, ty = _dtype_code(x), x.dtype
+    if conv_weight is not None and conv_weight.dim() != 3:
+        raise ValueError("conv_weight: expected [H,D,W]")
+    W = conv_weight.shape[-1] if conv_weight is not None else 0
+    if W == 0 and (conv_weight is not None or conv_state_in is not None or conv_state_out is not None):
+        raise ValueError("a convolution's state needs conv_weight [H,D,W] with W >= 1")
+    seq, group, state, chan = (B, H, T, D), (B, G, T, N), (B, H, D, N), (H, D)
+    cstate = (B, H, W - 1, D)
+    a = SsmArgs(B, H, G, T, D, N, W, code, GATES[gates], int(bool(conv_silu)),
+                _arg(x, "x", seq, ty, dev), _arg(dt, "dt", seq, ty, dev), _arg(Bm, "Bm", group, ty, dev),
+                _arg(Cm, "Cm", group, ty, dev), _arg(z, "z", seq, ty, dev), _arg(A, "A", (H, D, N), _F32, dev),
+                _arg(dt_bias, "dt_bias", chan, _F32, dev), _arg(feedthrough, "feedthrough", chan, _F32, dev),
+                _arg(conv_weight, "conv_weight", (H, D, W), _F32, dev), _arg(conv_bias, "conv_bias", chan, _F32, dev),
+                _arg(conv_state_in, "conv_state_in", cstate, ty, dev), _arg(S0, "S0", state, _F32, dev),
+                _arg(lengths, "lengths", (B,), torch.int32, dev), _arg(y, "y", seq, ty, dev),
+                _arg(ST, "ST", state, _F32, dev), _arg(conv_state_out, "conv_state_out", cstate, ty, dev),
+                _arg(saved_states, "saved_states", (B, H, (T + 15) // 16, D, N), _F32, dev), None, 0)
+    return a
+
+
+def _ssm_size(fn, a, where) -> int:
+    n = fn(ctypes.byref(a))
+    if n == ctypes.c_size_t(-1).value:
+        raise RdmError(RDM_ERR_INVALID_ARG, where)
+    return int(n)
+
+
+def rdm_ssm_saved_states_size(B, H, T, D, N) -> int:
+    return int(load().rdm_ssm_saved_states_size(B, H, T, D, N))
+
+
+def rdm_ssm_saved_states(x, A):
+    """A buffer [B,H,ceil(T/16),D,N] for the states that rdm_ssm_fwd saves for
+    rdm_ssm_bwd."""
+    B, H, T, D = x.shape
+    return torch.empty(B, H, (T + 15) // 16, D, A.shape[-1], dtype=_F32, device=x.device)
+
+
+def rdm_ssm_fwd_workspace_size(x, dt, A, Bm, Cm, *, conv_weight=None, gates="preact") -> int:
+    a = _ssm_args(x, dt, A, Bm, Cm, None, None, None, None, conv_weight, None, None, True, None, gates,
+                  None, None, None, None)
+    return _ssm_size(load().rdm_ssm_fwd_workspace_size, a, "rdm_ssm_fwd_workspace_size")
+
+
+def rdm_ssm_fwd(x, dt, A, Bm, Cm, *, S0=None, z=None, dt_bias=None, feedthrough=None, conv_weight=None,
+                conv_bias=None, conv_state_in=None, conv_silu=True, lengths=None, gates="preact", y=None,
+                ST=None, conv_state_out=None, saved_states=None, return_state=False, workspace=None,
+                stream=None):
+    """Selective state space scan over [B,H,T,D] sequences (include/rdm_ddts.h):
+    x, dt, z [B,H,T,D] and Bm, Cm [B,G,T,N] in one dtype, A [H,D,N], dt_bias,
+    feedthrough [H,D] float32; with conv_weight [H,D,W] (conv_bias [H,D],
+    conv_state_in [B,H,W-1,D]) x first goes through the causal convolution and,
+    unless conv_silu is False, its SiLU.  lengths [B] int32: tokens of each
+    sequence, rows of y behind them are left as they were (a y that is
+    allocated here starts with zeros then).  return_state allocates ST and
+    conv_state_out; workspace=False runs without one.  Returns (y, ST or None,
+    conv_state_out or None)."""
+    with _on(stream):
+        if y is None:
+            y = torch.empty_like(x) if lengths is None else torch.zeros_like(x)
+        if return_state and ST is None:
+            ST = torch.empty(x.shape[0], *A.shape, dtype=_F32, device=x.device)
+        if return_state and conv_state_out is None and conv_weight is not None:
+            B, H, _, D = x.shape
+            conv_state_out = torch.empty(B, H, conv_weight.shape[-1] - 1, D, dtype=x.dtype, device=x.device)
+        a = _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
+                      conv_silu, lengths, gates, y, ST, conv_state_out, saved_states)
+        if workspace is None:
+            need = _ssm_size(load().rdm_ssm_fwd_workspace_size, a, "rdm_ssm_fwd")
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        if workspace is not None and workspace is not False:
+            a.workspace, a.workspace_bytes = _buffer(workspace, "workspace", x.device)
+        _check(load().rdm_ssm_fwd(ctypes.byref(a), _stream(stream)), "rdm_ssm_fwd")
+    return y, ST, conv_state_out
+
+
+def _ssm_bwd_args(a, grad_y, grad_ST, grad_conv_state_out, g, dev):
+    seq, state = (a.B, a.H, a.T, a.D), (a.B, a.H, a.D, a.N)
+    group, chan, cstate = (a.B, a.G, a.T, a.N), (a.H, a.D), (a.B, a.H, a.W - 1, a.D)
+    ty = torch.bfloat16 if a.dtype == RDM_BF16 else _F32
+    if a.W == 0 and grad_conv_state_out is not None:
+        raise ValueError("a convolution's state needs conv_weight [H,D,W] with W >= 1")
+    return SsmBwdArgs(a, _arg(grad_y, "grad_y", seq, ty, dev), _arg(grad_ST, "grad_ST", state, _F32, dev),
+                      _arg(grad_conv_state_out, "grad_conv_state_out", cstate, ty, dev),
+                      _arg(g.get("dx"), "dx", seq, ty, dev), _arg(g.get("ddt"), "ddt", seq, ty, dev),
+                      _arg(g.get("dz"), "dz", seq, ty, dev), _arg(g.get("dB"), "dB", group, ty, dev),
+                      _arg(g.get("dC"), "dC", group, ty, dev), _arg(g.get("dA"), "dA", (a.H, a.D, a.N), _F32, dev),
+                      _arg(g.get("ddt_bias"), "ddt_bias", chan, _F32, dev), _arg(g.get("dfeed"), "dfeed", chan, _F32, dev),
+                      _arg(g.get("dconv_weight"), "dconv_weight", (a.H, a.D, a.W), _F32, dev),
+                      _arg(g.get("dconv_bias"), "dconv_bias", chan, _F32, dev), _arg(g.get("dS0"), "dS0", state, _F32, dev),
+                      _arg(g.get("dconv_state_in"), "dconv_state_in", cstate, ty, dev))
+
+
+def rdm_ssm_bwd_workspace_size(x, dt, A, Bm, Cm, saved_states=None, *, conv_weight=None, gates="preact") -> int:
+    a = _ssm_args(x, dt, A, Bm, Cm, None, None, None, None, conv_weight, None, None, True, None, gates,
+                  None, None, None, saved_states)
+    return _ssm_size(load().rdm_ssm_bwd_workspace_size, SsmBwdArgs(a), "rdm_ssm_bwd_workspace_size")
+
+
+def rdm_ssm_bwd(x, dt, A, Bm, Cm, grad_y, grad_ST=None, grad_conv_state_out=None, *, S0=None, z=None,
+                dt_bias=None, feedthrough=None, conv_weight=None, conv_bias=None, conv_state_in=None,
+                conv_silu=True, lengths=None, gates="preact", saved_states=None, grads=None, workspace=None,
+                stream=None):
+    """Reverse mode of rdm_ssm_fwd with the same arguments.  `grads` may hold
+    preallocated dx, ddt, dz, dB, dC, dA, ddt_bias, dfeed, dconv_weight,
+    dconv_bias, dconv_state_in, dS0; those whose input is given are allocated
+    with torch if missing, the others are None.  saved_states: the forward's
+    (None runs its recurrence again).  Returns the dict."""
+    with _on(stream):
+        g = dict(grads or {})
+        refs = [("dx", x), ("ddt", dt), ("dz", z), ("dB", Bm), ("dC", Cm), ("dA", A), ("ddt_bias", dt_bias),
+                ("dfeed", feedthrough), ("dconv_weight", conv_weight), ("dconv_bias", conv_bias),
+                ("dconv_state_in", conv_state_in), ("dS0", S0)]
+        for n, ref in refs:
+            if g.get(n) is None:
+                g[n] = torch.empty_like(ref) if ref is not None else None
+        a = _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
+                      conv_silu, lengths, gates, None, None, None, saved_states)
+        if a.W == 0 and (g["dconv_weight"] is not None or g["dconv_state_in"] is not None):
+            raise ValueError("gradients of a convolution need conv_weight [H,D,W] with W >= 1")
+        if not isinstance(grad_y, torch.Tensor):
+            raise TypeError("grad_y: expected a torch.Tensor")
+        ba = _ssm_bwd_args(a, grad_y, grad_ST, grad_conv_state_out, g, x.device)
+        if workspace is None:
+            need = _ssm_size(load().rdm_ssm_bwd_workspace_size, ba, "rdm_ssm_bwd")
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        if workspace is not None:
+            ba.fwd.workspace, ba.fwd.workspace_bytes = _buffer(workspace, "workspace", x.device)
+        _check(load().rdm_ssm_bwd(ctypes.byref(ba), _stream(stream)), "rdm_ssm_bwd")
+    return g
+
+
+def rdm_ssm_step(x, dt, A, Bm, Cm, S, *, z=None, dt_bias=None, feedthrough=None, conv_weight=None,
+                 conv_bias=None, conv_state=None, conv_silu=True, gates="preact", y=None, stream=None):
+    """One token of the selective scan: x, dt, z [B,H,D], Bm, Cm [B,G,N]; S
+    [B,H,D,N] float32 and conv_state [B,H,W-1,D] are updated in place.  Returns
+    y [B,H,D]."""
+    dev = _current(x)
+    if x.dim() != 3 or A.dim() != 3 or Bm.dim() != 3:
+        raise ValueError("x: expected [B,H,D], A: [H,D,N], Bm: [B,G,N]")
+    B, H, D = x.shape
+    N, G = A.shape[-1], Bm.shape[1]
+    W = conv_weight.shape[-1] if conv_weight is not None else 0
+    ty, chan = x.dtype, (H, D)
+    if conv_state is not None and W < 1:
+        raise ValueError("a convolution's state needs conv_weight [H,D,W] with W >= 1")
+    with _on(stream):
+        if y is None:
+            y = torch.empty_like(x)
+        a = SsmStepArgs(B, H, G, D, N, W, _dtype_code(x), GATES[gates], int(bool(conv_silu)),
+                        _arg(x, "x", (B, H, D), ty, dev), _arg(dt, "dt", (B, H, D), ty, dev),
+                        _arg(Bm, "Bm", (B, G, N), ty, dev), _arg(Cm, "Cm", (B, G, N), ty, dev),
+                        _arg(z, "z", (B, H, D), ty, dev), _arg(A, "A", (H, D, N), _F32, dev),
+                        _arg(dt_bias, "dt_bias", chan, _F32, dev), _arg(feedthrough, "feedthrough", chan, _F32, dev),
+                        _arg(conv_weight, "conv_weight", (H, D, W), _F32, dev),
+                        _arg(conv_bias, "conv_bias", chan, _F32, dev), _arg(S, "S", (B, H, D, N), _F32, dev),
+                        _arg(conv_state, "conv_state", (B, H, W - 1, D), ty, dev) if W > 1 else None,
+                        _arg(y, "y", (B, H, D), ty, dev))
+        _check(load().rdm_ssm_step(ctypes.byref(a), _stream(stream)), "rdm_ssm_step")
+    return y
 
 
 def rdm_ddts_sync_status(stream=None) -> int:

@@ -11,6 +11,7 @@
 #include "launch.h"
 #include "rdm_common.cuh"
 #include "ska_launch.h"
+#include "ssm_launch.h"
 
 namespace rdm {
 
@@ -464,6 +465,164 @@ rdm_status rdm_ska_decode(const rdm_ska_decode_args* a, rdm_stream_t stream) {
     return from_cuda(launch_ska_decode(p, static_cast<cudaStream_t>(stream)));
 }
 
+static bool ssm_dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+
+static rdm_status ssm_check(const rdm_ssm_args* a) {
+    if (!a || a->B < 1 || a->H < 1 || a->G < 1 || a->T < 0 || a->W < 0 || a->H % a->G != 0)
+        return RDM_ERR_INVALID_ARG;
+    if ((a->dtype != RDM_F32 && a->dtype != RDM_BF16) || !gates_ok(a->gate_inputs)) return RDM_ERR_INVALID_ARG;
+    if (!ssm_dim_ok(a->D) || !ssm_dim_ok(a->N) || a->W > 4) return RDM_ERR_UNSUPPORTED;
+    // blocks of eight channels or more fit a grid, element offsets 63 bits
+    if ((double)a->B * a->H * a->D > 8.0e9 || a->T > (1 << 30)) return RDM_ERR_INVALID_ARG;
+    if (!a->A || !aligned(a->A) || (a->W > 0) != (a->conv_weight != nullptr)) return RDM_ERR_INVALID_ARG;
+    if (a->T > 0) {
+        const void* in[] = {a->x, a->dt, a->Bm, a->Cm};
+        for (const void* p : in)
+            if (!p || !aligned(p)) return RDM_ERR_INVALID_ARG;
+    }
+    const void* opt[] = {a->z, a->dt_bias, a->feedthrough, a->conv_weight, a->conv_bias, a->conv_state_in, a->S0,
+                         a->saved_states, a->workspace};
+    for (const void* p : opt)
+        if (!opt_aligned(p)) return RDM_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(a->lengths) & 3u) != 0) return RDM_ERR_INVALID_ARG;
+    if (a->W == 0 && (a->conv_bias || a->conv_state_in)) return RDM_ERR_INVALID_ARG;
+    if (a->dt_bias && a->gate_inputs != RDM_GATES_PREACT) return RDM_ERR_INVALID_ARG;
+    return RDM_OK;
+}
+
+static SsmParams ssm_params(const rdm_ssm_args* a) {
+    SsmParams p;
+    memset(&p, 0, sizeof(p));
+    p.B = a->B; p.H = a->H; p.G = a->G; p.T = a->T; p.D = a->D; p.N = a->N; p.W = a->W;
+    p.bf16 = a->dtype == RDM_BF16;
+    p.preact = a->gate_inputs == RDM_GATES_PREACT;
+    p.silu = a->conv_silu != 0;
+    p.x = a->x; p.dt = a->dt; p.Bm = a->Bm; p.Cm = a->Cm; p.z = a->z;
+    p.A = a->A; p.dt_bias = a->dt_bias; p.dfeed = a->feedthrough;
+    p.cw = a->conv_weight; p.cb = a->conv_bias;
+    p.cs_in = a->W > 1 ? a->conv_state_in : nullptr;
+    p.S0 = a->S0; p.lengths = a->lengths;
+    p.y = a->y; p.ST = a->ST;
+    p.cs_out = a->W > 1 ? a->conv_state_out : nullptr;
+    p.saved = a->saved_states;
+    p.ws = a->workspace;
+    p.ws_bytes = a->workspace ? a->workspace_bytes : 0;
+    return p;
+}
+
+size_t rdm_ssm_saved_states_size(int B, int H, int T, int D, int N) {
+    if (B < 1 || H < 1 || T < 0 || !ssm_dim_ok(D) || !ssm_dim_ok(N)) return 0;
+    return (size_t)B * H * ((size_t)(T + kSsmChunk - 1) / kSsmChunk) * D * N * 4;
+}
+
+size_t rdm_ssm_fwd_workspace_size(const rdm_ssm_args* a) {
+    if (ssm_check(a) != RDM_OK) return (size_t)-1;
+    return ssm_fwd_workspace(ssm_params(a));
+}
+
+rdm_status rdm_ssm_fwd(const rdm_ssm_args* a, rdm_stream_t stream) {
+    rdm_status st = ssm_check(a);
+    if (st != RDM_OK) return st;
+    if ((a->T > 0 && !a->y) || !opt_aligned(a->y) || !opt_aligned(a->ST) || !opt_aligned(a->conv_state_out))
+        return RDM_ERR_INVALID_ARG;
+    if (a->W == 0 && a->conv_state_out) return RDM_ERR_INVALID_ARG;
+    SsmParams p = ssm_params(a);
+    p.err = status_word();
+    if (!p.err) return RDM_ERR_CUDA;
+    return from_cuda(launch_ssm_fwd(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static SsmBwdParams ssm_bwd_params(const rdm_ssm_bwd_args* a) {
+    SsmBwdParams p;
+    memset(&p, 0, sizeof(p));
+    p.f = ssm_params(&a->fwd);
+    p.f.y = nullptr;
+    p.f.ST = nullptr;
+    p.f.cs_out = nullptr;
+    p.gy = a->grad_y; p.gST = a->grad_ST;
+    p.gcs = a->fwd.W > 1 ? a->grad_conv_state_out : nullptr;
+    p.dx = a->grad_x; p.ddt = a->grad_dt; p.dz = a->fwd.z ? a->grad_z : nullptr;
+    p.dB = a->grad_B; p.dC = a->grad_C; p.dA = a->grad_A;
+    p.ddt_bias = a->grad_dt_bias; p.ddfeed = a->grad_feedthrough;
+    p.dcw = a->grad_conv_weight; p.dcb = a->grad_conv_bias;
+    p.dS0 = a->grad_S0;
+    p.dcs = a->fwd.W > 1 ? a->grad_conv_state_in : nullptr;
+    return p;
+}
+
+size_t rdm_ssm_bwd_workspace_size(const rdm_ssm_bwd_args* a) {
+    if (!a || ssm_check(&a->fwd) != RDM_OK) return (size_t)-1;
+    return a->fwd.T > 0 ? ssm_bwd_workspace(ssm_bwd_params(a)) : 0;
+}
+
+rdm_status rdm_ssm_bwd(const rdm_ssm_bwd_args* a, rdm_stream_t stream) {
+    if (!a) return RDM_ERR_INVALID_ARG;
+    rdm_status st = ssm_check(&a->fwd);
+    if (st != RDM_OK) return st;
+    const rdm_ssm_args& f = a->fwd;
+    const void* opt[] = {a->grad_ST, a->grad_conv_state_out, a->grad_z, a->grad_dt_bias, a->grad_feedthrough,
+                         a->grad_conv_weight, a->grad_conv_bias, a->grad_S0, a->grad_conv_state_in};
+    for (const void* p : opt)
+        if (!opt_aligned(p)) return RDM_ERR_INVALID_ARG;
+    if (!a->grad_A || !aligned(a->grad_A)) return RDM_ERR_INVALID_ARG;
+    if (f.T > 0) {
+        const void* out[] = {a->grad_y, a->grad_x, a->grad_dt, a->grad_B, a->grad_C};
+        for (const void* p : out)
+            if (!p || !aligned(p)) return RDM_ERR_INVALID_ARG;
+        if (f.z && !a->grad_z) return RDM_ERR_INVALID_ARG;
+    }
+    if ((a->grad_dt_bias && f.gate_inputs != RDM_GATES_PREACT) || (a->grad_feedthrough && !f.feedthrough) ||
+        (f.W == 0 && (a->grad_conv_weight || a->grad_conv_bias || a->grad_conv_state_in || a->grad_conv_state_out)))
+        return RDM_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    SsmBwdParams p = ssm_bwd_params(a);
+    if (f.T == 0) {  // no tokens: the carried gradients pass through, the weights have none
+        const size_t hd = (size_t)f.H * f.D, states = (size_t)f.B * hd * f.N * 4;
+        const size_t inputs = f.W > 1 ? (size_t)f.B * hd * (f.W - 1) * (p.f.bf16 ? 2 : 4) : 0;
+        const struct { void* out; const void* in; size_t n; } pass[] = {
+            {p.dS0, p.gST, states}, {p.dcs, p.gcs, inputs}, {p.dA, nullptr, hd * f.N * 4},
+            {p.ddt_bias, nullptr, hd * 4}, {p.ddfeed, nullptr, hd * 4}, {p.dcw, nullptr, hd * f.W * 4}, {p.dcb, nullptr, hd * 4}};
+        for (const auto& c : pass) {
+            if (!c.out || !c.n) continue;
+            const cudaError_t e = c.in ? cudaMemcpyAsync(c.out, c.in, c.n, cudaMemcpyDeviceToDevice, s)
+                                       : cudaMemsetAsync(c.out, 0, c.n, s);
+            if (e != cudaSuccess) return RDM_ERR_CUDA;
+        }
+        return RDM_OK;
+    }
+    const size_t need = ssm_bwd_workspace(p);
+    if (!p.f.ws || p.f.ws_bytes < need) return RDM_ERR_WORKSPACE;
+    p.f.err = status_word();
+    if (!p.f.err) return RDM_ERR_CUDA;
+    return from_cuda(launch_ssm_bwd(p, s));
+}
+
+rdm_status rdm_ssm_step(const rdm_ssm_step_args* a, rdm_stream_t stream) {
+    if (!a || a->B < 1 || a->H < 1 || a->G < 1 || a->W < 0 || a->H % a->G != 0) return RDM_ERR_INVALID_ARG;
+    if ((a->dtype != RDM_F32 && a->dtype != RDM_BF16) || !gates_ok(a->gate_inputs)) return RDM_ERR_INVALID_ARG;
+    if (!ssm_dim_ok(a->D) || !ssm_dim_ok(a->N) || a->W > 4) return RDM_ERR_UNSUPPORTED;
+    if ((double)a->B * a->H * a->D > 8.0e9) return RDM_ERR_INVALID_ARG;
+    const void* in[] = {a->x, a->dt, a->Bm, a->Cm, a->A, a->S, a->y};
+    for (const void* p : in)
+        if (!p || !aligned(p)) return RDM_ERR_INVALID_ARG;
+    const void* opt[] = {a->z, a->dt_bias, a->feedthrough, a->conv_weight, a->conv_bias, a->conv_state};
+    for (const void* p : opt)
+        if (!opt_aligned(p)) return RDM_ERR_INVALID_ARG;
+    if ((a->W > 0) != (a->conv_weight != nullptr) || (a->W > 1) != (a->conv_state != nullptr) ||
+        (a->W == 0 && a->conv_bias) || (a->dt_bias && a->gate_inputs != RDM_GATES_PREACT))
+        return RDM_ERR_INVALID_ARG;
+    SsmStepParams p;
+    memset(&p, 0, sizeof(p));
+    p.B = a->B; p.H = a->H; p.G = a->G; p.D = a->D; p.N = a->N; p.W = a->W;
+    p.bf16 = a->dtype == RDM_BF16;
+    p.preact = a->gate_inputs == RDM_GATES_PREACT;
+    p.silu = a->conv_silu != 0;
+    p.x = a->x; p.dt = a->dt; p.Bm = a->Bm; p.Cm = a->Cm; p.z = a->z;
+    p.A = a->A; p.dt_bias = a->dt_bias; p.dfeed = a->feedthrough; p.cw = a->conv_weight; p.cb = a->conv_bias;
+    p.S = a->S; p.cs = a->conv_state; p.y = a->y;
+    return from_cuda(launch_ssm_step(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 rdm_status rdm_ddts_sync_status(rdm_stream_t stream) {
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return RDM_ERR_CUDA;
@@ -501,6 +660,6 @@ rdm_status rdm_ddts_set_test_hooks(long long wait_limit_cycles, int withhold_seg
     return RDM_OK;
 }
 
-int rdm_ddts_version(void) { return 700; }
+int rdm_ddts_version(void) { return 800; }
 
 }  // extern "C"

@@ -1,0 +1,381 @@
+// ssm.cu -- selective state space scan (Gu and Dao, "Mamba: Linear-Time Sequence
+// Modeling with Selective State Spaces", arXiv 2312.00752, Section 3) with its
+// short causal convolution, for prompts and for single tokens.  Per channel
+// (h, c), state n, token t, the head's group g:
+//
+//   u_t = silu(bias + sum_{i<W} w_i x_{t-i})   (x_t itself without a convolution)
+//   delta_t = softplus(dt_t + dt_bias)
+//   s_t[n] = exp(delta_t A[n]) s_{t-1}[n] + delta_t u_t B_t[n]
+//   y_t = (sum_n C_t[n] s_t[n] + d u_t) silu(z_t)
+//
+// The decays differ by channel and state, so there is no matrix product in it:
+// the recurrence runs on the CUDA cores in float32, and its floor is the
+// exponential unit (one ex2 per channel, token and state; 16 a clock and SM).
+//
+// Forward: a block has CPB channels of one (b, h), four states a thread, and
+// walks its tokens in tiles of 32.  Threads first make delta and u of the tile
+// (two channels by four tokens a thread) in shared memory, then run the
+// recurrence, sums over n by shuffles for four tokens at a time, then finish y
+// with the skip and the gate in the same layout as the loads.  Where the
+// channels alone do not fill the card, each sequence is cut into P segments: a
+// first launch runs every segment but the last from a zero state and leaves its
+// end state and its sum of delta; in the second each block folds the segments
+// before its own, s <- local + exp(A sum delta) s, and runs for good.
+#include "launch.h"
+#include "ssm_common.cuh"
+
+namespace rdm {
+namespace {
+
+using namespace ssm;
+
+constexpr int kTile = 32;
+
+// Segments of a scan: `len` tokens each (a multiple of kTile); local[seg][b][h][D][N]
+// and dsum[seg][b][h][D] from the first launch.
+struct SegArgs {
+    int P, len;
+    float *local, *dsum;
+};
+
+template <typename T, int N, int CPB, bool LOCAL>
+__global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p, const SegArgs sg) {
+    using L = Lay<N, CPB>;
+    constexpr int LPC = L::LPC, TH = L::THREADS, UNITS = (kTile / 4) * (CPB / 2);
+    __shared__ __align__(16) float sD[kTile / 4][L::PLACES][4];
+    __shared__ __align__(16) float sU[kTile / 4][L::PLACES][4];
+    __shared__ __align__(16) float sY[kTile / 4][L::PLACES][4];
+    __shared__ __align__(16) float sB[kTile][N];
+    __shared__ __align__(16) float sC[LOCAL ? 1 : kTile][N];
+    const int nblk = p.D / CPB;
+    const int bh = blockIdx.x / nblk, c0 = (blockIdx.x % nblk) * CPB;
+    const int b = bh / p.H, h = bh % p.H, seg = blockIdx.y;
+    const int len = seq_len(p, b);
+    const int begin = seg * sg.len;
+    if (LOCAL ? begin + sg.len >= len : (seg > 0 && begin >= len)) return;  // nothing after or in it
+    const int end = LOCAL ? begin + sg.len : min(begin + sg.len, len);
+    const bool last = end == len;
+    const int tid = threadIdx.x;
+    const size_t row0 = (size_t)bh * p.T;
+    const T* x = static_cast<const T*>(p.x) + row0 * p.D + c0;
+    const T* dt = static_cast<const T*>(p.dt) + row0 * p.D + c0;
+    const T* z = p.z ? static_cast<const T*>(p.z) + row0 * p.D + c0 : nullptr;
+    T* y = static_cast<T*>(p.y) + row0 * p.D + c0;
+    const size_t grow = (size_t)(b * p.G + h / (p.H / p.G)) * p.T;
+    const T* Bm = static_cast<const T*>(p.Bm) + grow * N;
+    const T* Cm = static_cast<const T*>(p.Cm) + grow * N;
+    const T* cs = p.cs_in ? static_cast<const T*>(p.cs_in) + (size_t)bh * (p.W - 1) * p.D + c0 : nullptr;
+
+    // the recurrence's part of this thread: states 4 sl .. 4 sl + 3 of channel ch
+    const int ch = tid / LPC, sl = tid % LPC;
+    const size_t srow = ((size_t)bh * p.D + c0 + ch) * N + 4 * sl;
+    float A2[4], s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dsum = 0.0f;
+    {
+        const float4 a = ld4(p.A + ((size_t)h * p.D + c0 + ch) * N + 4 * sl);
+        A2[0] = a.x * kLog2e; A2[1] = a.y * kLog2e; A2[2] = a.z * kLog2e; A2[3] = a.w * kLog2e;
+    }
+    if (!LOCAL) {
+        if (p.S0) {
+            const float4 v = ld4(p.S0 + srow);
+            s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
+        }
+        const size_t states = (size_t)p.B * p.H * p.D;
+        for (int j = 0; j < seg; ++j) {  // the segments before this one
+            const float4 v = *reinterpret_cast<const float4*>(sg.local + j * states * N + srow);
+            const float ds = sg.dsum[j * states + (size_t)bh * p.D + c0 + ch];
+            s[0] = fmaf(ex2_fast(A2[0] * ds), s[0], v.x);
+            s[1] = fmaf(ex2_fast(A2[1] * ds), s[1], v.y);
+            s[2] = fmaf(ex2_fast(A2[2] * ds), s[2], v.z);
+            s[3] = fmaf(ex2_fast(A2[3] * ds), s[3], v.w);
+        }
+    }
+    // the element-wise part: channels cp, cp + 1 of tokens 4 uq .. 4 uq + 3
+    const int cp = 2 * (tid % (CPB / 2)), pl = cp >> 1;
+    float w[4][2] = {}, cb[2] = {0.0f, 0.0f}, bias[2] = {0.0f, 0.0f}, feed[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int hc = h * p.D + c0 + cp + e;
+        for (int i = 0; i < p.W; ++i) w[i][e] = p.cw[(size_t)hc * p.W + i];
+        if (p.cb) cb[e] = p.cb[hc];
+        if (p.dt_bias) bias[e] = p.dt_bias[hc];
+        if (p.dfeed) feed[e] = p.dfeed[hc];
+    }
+
+    for (int t0 = begin; t0 < end; t0 += kTile) {
+        for (int unit = tid; unit < UNITS; unit += TH) {
+            const int q = unit / (CPB / 2), tq = t0 + 4 * q;
+            float2 xv[7];
+#pragma unroll
+            for (int i = 0; i < 7; ++i) {
+                const int t = tq - 3 + i;
+                xv[i] = make_float2(0.0f, 0.0f);
+                if (i < 3 && p.W < 4 - i) continue;  // 3 - i tokens back: not in the filter
+                if (t >= 0) {
+                    if (t < end) xv[i] = Pair<T>::f(ldpair(x + (size_t)t * p.D + cp));
+                } else if (cs && t >= 1 - p.W) {
+                    xv[i] = Pair<T>::f(ldpair(cs + (size_t)(p.W - 1 + t) * p.D + cp));
+                }
+            }
+            float du[2][4], uu[2][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool live = tq + j < end;
+                float2 d = make_float2(0.0f, 0.0f);
+                if (live) d = Pair<T>::f(ldpair(dt + (size_t)(tq + j) * p.D + cp));
+                float u0 = xv[3 + j].x, u1 = xv[3 + j].y;
+                if (p.W) {
+                    float z0 = cb[0], z1 = cb[1];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < p.W) {
+                            z0 = fmaf(w[i][0], xv[3 + j - i].x, z0);
+                            z1 = fmaf(w[i][1], xv[3 + j - i].y, z1);
+                        }
+                    u0 = p.silu ? silu(z0) : z0;
+                    u1 = p.silu ? silu(z1) : z1;
+                }
+                if (p.preact) {
+                    d.x = softplus(d.x + bias[0]);
+                    d.y = softplus(d.y + bias[1]);
+                }
+                // tokens behind the end leave the state as it is
+                du[0][j] = live ? d.x : 0.0f;
+                du[1][j] = live ? d.y : 0.0f;
+                uu[0][j] = live ? u0 : 0.0f;
+                uu[1][j] = live ? u1 : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                *reinterpret_cast<float4*>(sD[q][pl + e * L::ODD]) = make_float4(du[e][0], du[e][1], du[e][2], du[e][3]);
+                *reinterpret_cast<float4*>(sU[q][pl + e * L::ODD]) = make_float4(uu[e][0], uu[e][1], uu[e][2], uu[e][3]);
+            }
+        }
+        for (int i = tid; i < kTile * N / 4; i += TH) {
+            const int t = t0 + i / (N / 4), n = 4 * (i % (N / 4));
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = v;
+            if (t < end) {
+                v = ld4(Bm + (size_t)t * N + n);
+                if (!LOCAL) u = ld4(Cm + (size_t)t * N + n);
+            }
+            *reinterpret_cast<float4*>(&sB[t - t0][n]) = v;
+            if (!LOCAL) *reinterpret_cast<float4*>(&sC[t - t0][n]) = u;
+        }
+        __syncthreads();
+        const int place = L::place(ch);
+#pragma unroll 1
+        for (int q = 0; q < kTile / 4; ++q) {
+            if (!LOCAL && p.saved && (q & 3) == 0 && t0 + 4 * q < end) {
+                const size_t nc = (p.T + kSsmChunk - 1) / kSsmChunk;
+                const size_t at = (((size_t)bh * nc + (t0 + 4 * q) / kSsmChunk) * p.D + c0 + ch) * N + 4 * sl;
+                *reinterpret_cast<float4*>(p.saved + at) = make_float4(s[0], s[1], s[2], s[3]);
+            }
+            const float4 d4 = *reinterpret_cast<const float4*>(sD[q][place]);
+            const float4 u4 = *reinterpret_cast<const float4*>(sU[q][place]);
+            const float dd[4] = {d4.x, d4.y, d4.z, d4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
+            float yy[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 bb = *reinterpret_cast<const float4*>(&sB[4 * q + j][4 * sl]);
+                const float du = dd[j] * uu[j];
+                s[0] = fmaf(ex2_fast(dd[j] * A2[0]), s[0], du * bb.x);
+                s[1] = fmaf(ex2_fast(dd[j] * A2[1]), s[1], du * bb.y);
+                s[2] = fmaf(ex2_fast(dd[j] * A2[2]), s[2], du * bb.z);
+                s[3] = fmaf(ex2_fast(dd[j] * A2[3]), s[3], du * bb.w);
+                if (LOCAL) {
+                    dsum += dd[j];
+                } else {
+                    const float4 cc = *reinterpret_cast<const float4*>(&sC[4 * q + j][4 * sl]);
+                    yy[j] = fmaf(s[0], cc.x, fmaf(s[1], cc.y, fmaf(s[2], cc.z, s[3] * cc.w)));
+                }
+            }
+            if (!LOCAL) {
+                const float r = lane_sum4<LPC>(yy[0], yy[1], yy[2], yy[3]);
+                if (sl < 4) sY[q][place][sl] = r;
+            }
+        }
+        __syncthreads();
+        if (!LOCAL && p.y) {
+            for (int unit = tid; unit < UNITS; unit += TH) {
+                const int q = unit / (CPB / 2), tq = t0 + 4 * q;
+                float yv[2][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float4 a = *reinterpret_cast<const float4*>(sY[q][pl + e * L::ODD]);
+                    const float4 u = *reinterpret_cast<const float4*>(sU[q][pl + e * L::ODD]);
+                    yv[e][0] = fmaf(feed[e], u.x, a.x); yv[e][1] = fmaf(feed[e], u.y, a.y);
+                    yv[e][2] = fmaf(feed[e], u.z, a.z); yv[e][3] = fmaf(feed[e], u.w, a.w);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (tq + j >= end) continue;
+                    float2 g = make_float2(1.0f, 1.0f);
+                    if (z) {
+                        g = Pair<T>::f(ldpair(z + (size_t)(tq + j) * p.D + cp));
+                        g.x = silu(g.x);
+                        g.y = silu(g.y);
+                    }
+                    stpair(y + (size_t)(tq + j) * p.D + cp, yv[0][j] * g.x, yv[1][j] * g.y);
+                }
+            }
+            // sU is written again by the threads that read it here; sY only behind the next barrier
+        }
+    }
+    if (LOCAL) {
+        const size_t states = (size_t)p.B * p.H * p.D;
+        *reinterpret_cast<float4*>(sg.local + seg * states * N + srow) = make_float4(s[0], s[1], s[2], s[3]);
+        if (sl == 0) sg.dsum[seg * states + (size_t)bh * p.D + c0 + ch] = dsum;
+        return;
+    }
+    if (!last) return;
+    if (p.ST) *reinterpret_cast<float4*>(p.ST + srow) = make_float4(s[0], s[1], s[2], s[3]);
+    if (p.cs_out) {  // the last W-1 inputs, some of them perhaps carried in
+        T* out = static_cast<T*>(p.cs_out) + (size_t)bh * (p.W - 1) * p.D + c0;
+        for (int i = tid; i < (p.W - 1) * CPB; i += TH) {
+            const int r = i / CPB, c = i % CPB, t = len - (p.W - 1) + r;
+            float v = 0.0f;
+            if (t >= 0) v = ldf(x + (size_t)t * p.D + c);
+            else if (cs) v = ldf(cs + (size_t)(p.W - 1 + t) * p.D + c);
+            stf(out + (size_t)r * p.D + c, v);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ single tokens
+constexpr int kStepThreads = 128;
+
+// One thread has four states of a channel; a channel's lanes share its inputs.
+// A pure stream of the state, read and written once.
+template <typename T, int N>
+__global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmStepParams p) {
+    constexpr int LPC = N / 4;
+    const size_t i = (size_t)blockIdx.x * kStepThreads + threadIdx.x;
+    const size_t rows = (size_t)p.B * p.H * p.D;
+    const bool live = i / LPC < rows;
+    const size_t row = live ? i / LPC : rows - 1;  // idle lanes follow the last channel and store nothing
+    const int sl = (int)(i % LPC);
+    const int c = (int)(row % p.D);
+    const int bh = (int)(row / p.D), b = bh / p.H, h = bh % p.H;
+    const int hc = h * p.D + c;
+    const float4 s4 = *reinterpret_cast<const float4*>(p.S + row * N + 4 * sl);
+    const float4 a4 = ld4(p.A + (size_t)hc * N + 4 * sl);
+    const size_t grow = (size_t)(b * p.G + h / (p.H / p.G)) * N + 4 * sl;
+    const float4 b4 = ld4(static_cast<const T*>(p.Bm) + grow), c4 = ld4(static_cast<const T*>(p.Cm) + grow);
+    const T* x = static_cast<const T*>(p.x);
+    float u = ldf(x + row), d = ldf(static_cast<const T*>(p.dt) + row);
+    if (p.W) {
+        T* cs = static_cast<T*>(p.cs) + (size_t)bh * (p.W - 1) * p.D + c;
+        const T xt = x[row];
+        T old[3];
+        float acc = fmaf(p.cw[(size_t)hc * p.W], u, p.cb ? p.cb[hc] : 0.0f);
+#pragma unroll
+        for (int k = 1; k < 4; ++k)
+            if (k < p.W) {
+                old[k - 1] = cs[(size_t)(p.W - 1 - k) * p.D];
+                acc = fmaf(p.cw[(size_t)hc * p.W + k], ldf(&old[k - 1]), acc);
+            }
+        u = p.silu ? silu(acc) : acc;
+        __syncwarp();  // every lane of the channel has read the old inputs
+        if (sl == 0 && live) {
+            if (p.W > 1) cs[(size_t)(p.W - 2) * p.D] = xt;
+#pragma unroll
+            for (int k = 1; k < 3; ++k)
+                if (k < p.W - 1) cs[(size_t)(p.W - 2 - k) * p.D] = old[k - 1];
+        }
+    }
+    if (p.preact) d = softplus(d + (p.dt_bias ? p.dt_bias[hc] : 0.0f));
+    const float d2 = d * kLog2e, du = d * u;
+    float4 s;
+    s.x = fmaf(ex2_fast(d2 * a4.x), s4.x, du * b4.x);
+    s.y = fmaf(ex2_fast(d2 * a4.y), s4.y, du * b4.y);
+    s.z = fmaf(ex2_fast(d2 * a4.z), s4.z, du * b4.z);
+    s.w = fmaf(ex2_fast(d2 * a4.w), s4.w, du * b4.w);
+    if (live) *reinterpret_cast<float4*>(p.S + row * N + 4 * sl) = s;
+    float y = fmaf(s.x, c4.x, fmaf(s.y, c4.y, fmaf(s.z, c4.z, s.w * c4.w)));
+#pragma unroll
+    for (int o = 1; o < LPC; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+    if (sl == 0 && live) {
+        if (p.dfeed) y = fmaf(p.dfeed[hc], u, y);
+        if (p.z) y *= silu(ldf(static_cast<const T*>(p.z) + row));
+        stf(static_cast<T*>(p.y) + row, y);
+    }
+}
+
+int channels_per_block(int D, int N) {
+    const int most = N == 16 ? 32 : N == 32 ? 16 : 8;
+    return D < most ? D : most;
+}
+
+// Segments that a sequence is cut into: 1 where the channels alone give every SM
+// four blocks (the first launch repeats the exponentials), else enough for that,
+// each of at least four tiles.
+int segments(const SsmParams& p) {
+    const long long blocks = (long long)p.B * p.H * (p.D / channels_per_block(p.D, p.N));
+    const long long want = 4LL * sm_count();
+    if (blocks * 2 > want) return 1;
+    long long P = want / blocks;
+    const long long most = p.T / (4 * kTile);
+    if (P > most) P = most;
+    if (P > 64) P = 64;
+    return P < 2 ? 1 : (int)P;
+}
+int segment_len(int T, int P) {
+    const int tiles = (T + kTile - 1) / kTile;
+    return (tiles + P - 1) / P * kTile;
+}
+
+template <typename T, int N, int CPB>
+cudaError_t launch_fwd(const SsmParams& p, const SegArgs& sg, cudaStream_t s) {
+    const unsigned blocks = (unsigned)((long long)p.B * p.H * (p.D / CPB));
+    if (sg.P > 1) {
+        ssm_fwd_kernel<T, N, CPB, true><<<dim3(blocks, sg.P - 1), CPB * N / 4, 0, s>>>(p, sg);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    ssm_fwd_kernel<T, N, CPB, false><<<dim3(blocks, sg.P), CPB * N / 4, 0, s>>>(p, sg);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_fwd_t(const SsmParams& p, const SegArgs& sg, cudaStream_t s) {
+    switch (p.N) {
+        case 16: return p.D >= 32 ? launch_fwd<T, 16, 32>(p, sg, s) : launch_fwd<T, 16, 16>(p, sg, s);
+        case 32: return launch_fwd<T, 32, 16>(p, sg, s);
+        case 64: return launch_fwd<T, 64, 8>(p, sg, s);
+        default: return launch_fwd<T, 128, 8>(p, sg, s);
+    }
+}
+
+template <typename T>
+cudaError_t launch_step_t(const SsmStepParams& p, cudaStream_t s) {
+    const long long threads = (long long)p.B * p.H * p.D * (p.N / 4);
+    const unsigned grid = (unsigned)((threads + kStepThreads - 1) / kStepThreads);
+    switch (p.N) {
+        case 16: ssm_step_kernel<T, 16><<<grid, kStepThreads, 0, s>>>(p); break;
+        case 32: ssm_step_kernel<T, 32><<<grid, kStepThreads, 0, s>>>(p); break;
+        case 64: ssm_step_kernel<T, 64><<<grid, kStepThreads, 0, s>>>(p); break;
+        default: ssm_step_kernel<T, 128><<<grid, kStepThreads, 0, s>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t ssm_fwd_workspace(const SsmParams& p) {
+    const int P = segments(p);
+    return P < 2 ? 0 : (size_t)(P - 1) * p.B * p.H * p.D * (p.N + 1) * 4;
+}
+
+cudaError_t launch_ssm_fwd(const SsmParams& p, cudaStream_t s) {
+    SegArgs sg;
+    sg.P = p.ws && p.ws_bytes >= ssm_fwd_workspace(p) ? segments(p) : 1;
+    sg.len = segment_len(p.T, sg.P);
+    sg.local = static_cast<float*>(p.ws);
+    sg.dsum = sg.local + (size_t)(sg.P - 1) * p.B * p.H * p.D * p.N;
+    return p.bf16 ? launch_fwd_t<__nv_bfloat16>(p, sg, s) : launch_fwd_t<float>(p, sg, s);
+}
+
+cudaError_t launch_ssm_step(const SsmStepParams& p, cudaStream_t s) {
+    return p.bf16 ? launch_step_t<__nv_bfloat16>(p, s) : launch_step_t<float>(p, s);
+}
+
+}  // namespace rdm

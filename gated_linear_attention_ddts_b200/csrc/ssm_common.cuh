@@ -1,0 +1,118 @@
+// ssm_common.cuh -- device pieces shared by the selective scan's forward, step
+// and backward: activations to float32 accuracy, channel pairs, thread layout.
+#pragma once
+
+#include "rdm_common.cuh"
+#include "ssm_launch.h"
+
+namespace rdm {
+namespace ssm {
+
+// softplus(x) = max(x, 0) + log1p(e^-|x|).  The steps sit near 1e-3..1e-1, where
+// the logarithm's argument is close to 1 and lg2.approx (absolute error 2^-22)
+// would leave only 12 of their bits; so log1p(y) = 2 atanh(s), s = y / (2 + y),
+// as 2 s P(s^2) with s^2 <= 1/9 (P fitted here, relative error 4e-9), which the
+// float32 states and gradients need.
+__device__ __forceinline__ float softplus(float x) {
+    const float y = ex2_fast(-fabsf(x) * kLog2e);
+    const float s = __fdividef(y, 2.0f + y);
+    const float q = s * s;
+    float r = 0.2817833423614502f;
+    r = fmaf(r, q, 0.27960604429244995f);
+    r = fmaf(r, q, 0.40024909377098083f);
+    r = fmaf(r, q, 0.6666631698608398f);
+    r = fmaf(r, q, 2.0f);
+    return x != x ? x : fmaf(s, r, fmaxf(x, 0.0f));
+}
+__device__ __forceinline__ float sigmoid(float x) {
+    return __fdividef(1.0f, 1.0f + ex2_fast(fminf(-x * kLog2e, 126.0f)));
+}
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+// d silu(x) / dx = s (1 + x (1 - s))
+__device__ __forceinline__ float dsilu(float x, float s) { return s * fmaf(x, 1.0f - s, 1.0f); }
+
+// Two neighbouring channels of a row.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+    using Raw = uint32_t;
+    static __device__ __forceinline__ Raw zero() { return 0u; }
+    static __device__ __forceinline__ float2 f(Raw r) {
+        return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+    }
+    static __device__ __forceinline__ Raw r(float a, float b) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<Raw*>(&h);
+    }
+};
+template <>
+struct Pair<float> {
+    using Raw = float2;
+    static __device__ __forceinline__ Raw zero() { return make_float2(0.0f, 0.0f); }
+    static __device__ __forceinline__ float2 f(Raw r) { return r; }
+    static __device__ __forceinline__ Raw r(float a, float b) { return make_float2(a, b); }
+};
+template <typename T>
+__device__ __forceinline__ typename Pair<T>::Raw ldpair(const T* p) {
+    return __ldg(reinterpret_cast<const typename Pair<T>::Raw*>(p));
+}
+template <typename T>
+__device__ __forceinline__ void stpair(T* p, float a, float b) {
+    *reinterpret_cast<typename Pair<T>::Raw*>(p) = Pair<T>::r(a, b);
+}
+// four neighbouring values as float32
+__device__ __forceinline__ float4 ld4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
+// Sums of four values over the LPC lanes of a channel (LPC >= 4 neighbouring
+// lanes): lane l ends with the sum of value l & 3.  Three shuffles for the first
+// four lanes instead of the eight of four separate sums.
+template <int LPC>
+__device__ __forceinline__ float lane_sum4(float a0, float a1, float a2, float a3) {
+    const int lane = threadIdx.x & 31;
+    const bool hi = lane & 2, odd = lane & 1;
+    const float s0 = hi ? a0 : a2, s1 = hi ? a1 : a3;
+    float k0 = hi ? a2 : a0, k1 = hi ? a3 : a1;
+    k0 += __shfl_xor_sync(0xffffffffu, s0, 2);
+    k1 += __shfl_xor_sync(0xffffffffu, s1, 2);
+    const float s = odd ? k0 : k1;
+    float k = odd ? k1 : k0;
+    k += __shfl_xor_sync(0xffffffffu, s, 1);
+#pragma unroll
+    for (int o = 4; o < LPC; o <<= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+    return k;
+}
+
+// Tokens of sequence b, 0..T; out of range sets the status word and counts as
+// the nearest end.
+__device__ __forceinline__ int seq_len(const SsmParams& p, int b) {
+    if (!p.lengths) return p.T;
+    const int n = p.lengths[b];
+    if (n < 0 || n > p.T) {
+        if (threadIdx.x == 0) atomicOr(p.err, 2u);  // kErrBadValue
+        return n < 0 ? 0 : p.T;
+    }
+    return n;
+}
+
+// Thread layout: each channel's N states lie on N/4 neighbouring lanes, four a
+// lane; a block has CPB channels of one head.
+template <int N, int CPB>
+struct Lay {
+    static constexpr int LPC = N / 4;
+    static constexpr int THREADS = CPB * LPC;
+    // Shared-memory place of channel c in the [token quad][place][4] arrays: even
+    // and odd channels apart, so that the threads that write pairs of channels
+    // and the lanes that read neighbouring ones both spread over the banks.
+    static constexpr int ODD = CPB / 2 + 4;
+    static constexpr int PLACES = CPB + 4;
+    static __device__ __forceinline__ int place(int c) { return (c >> 1) + (c & 1) * ODD; }
+};
+
+}  // namespace ssm
+}  // namespace rdm

@@ -414,6 +414,124 @@ typedef struct {
 
 rdm_status rdm_ska_decode(const rdm_ska_decode_args *args, rdm_stream_t stream);
 
+/* ------------------------------------------------------- selective scan
+ * Selective state space scan with its short causal convolution (Gu and Dao,
+ * "Mamba: Linear-Time Sequence Modeling with Selective State Spaces", arXiv
+ * 2312.00752, Section 3), the recurrence whose decay has a full [channel,
+ * state] matrix and an input-dependent step.  Channels are (head, channel)
+ * pairs as for the ShortConv; per channel (h, c), state n and token t, with g
+ * = h / (H/G) the head's group:
+ *
+ *   u_t     = silu(conv_bias + sum_{i<W} conv_weight[h,c,i] x_{t-i})   (W > 0)
+ *   u_t     = x_t                                                      (W = 0)
+ *   delta_t = softplus(dt_t + dt_bias)  (RDM_GATES_PREACT)  or  dt_t
+ *   s_t[n]  = exp(delta_t A[h,c,n]) s_{t-1}[n] + delta_t u_t B[b,g,t,n]
+ *   y_t     = (sum_n C[b,g,t,n] s_t[n] + feedthrough[h,c] u_t) silu(z_t)
+ *
+ *   x, dt, y      : [B,H,T,D] dtype        D in {16, 32, 64, 128}
+ *   Bm, Cm        : [B,G,T,N] dtype        N in {16, 32, 64, 128}; G divides H
+ *   z             : [B,H,T,D] dtype gate, or NULL for none
+ *   A             : [H,D,N] float32 (negative for a decay; not checked)
+ *   dt_bias       : [H,D] float32 or NULL (zero); PREACT only
+ *   feedthrough   : [H,D] float32 or NULL (none)
+ *   conv_weight   : [H,D,W] float32, W <= 4, NULL exactly when W = 0
+ *   conv_bias     : [H,D] float32 or NULL
+ *   conv_silu     : 0 leaves out the SiLU behind the convolution
+ *   conv_state_in : [B,H,W-1,D] dtype, the W-1 inputs before the sequence
+ *                   (oldest first), or NULL for zeros
+ *   S0            : [B,H,D,N] float32, or NULL for zero
+ *   lengths       : [B] int32 tokens of each sequence, 0..T, or NULL for T each.
+ *                   Tokens at and behind a sequence's length are not part of
+ *                   it: they are not used, y is left as it was there, and ST
+ *                   and conv_state_out are those of its last token.  A value
+ *                   out of range counts as the nearest end and makes
+ *                   rdm_ddts_sync_status return RDM_ERR_INVALID_ARG.
+ *   ST            : [B,H,D,N] float32 final state, written; NULL = skip
+ *   conv_state_out: [B,H,W-1,D] dtype, written; NULL = skip
+ *   saved_states  : [B,H,ceil(T/16),D,N] float32, written with the state before
+ *                   every 16 tokens for rdm_ssm_bwd; NULL = skip
+ *   workspace     : optional scratch; with rdm_ssm_fwd_workspace_size() bytes
+ *                   long sequences of few channels are cut into segments that
+ *                   run side by side.  Contents on entry are ignored; calls
+ *                   whose kernels may overlap must not share it.
+ * Arithmetic is float32 throughout, on either dtype.  Outputs must not alias
+ * inputs.  The result of a call is the same bits every time. */
+typedef struct {
+    int B, H, G, T, D, N, W;
+    rdm_dtype dtype;
+    rdm_gate_inputs gate_inputs;
+    int conv_silu;
+    const void *x, *dt, *Bm, *Cm, *z;
+    const float *A, *dt_bias, *feedthrough, *conv_weight, *conv_bias;
+    const void *conv_state_in;
+    const float *S0;
+    const int *lengths;
+    void *y;
+    float *ST;
+    void *conv_state_out;
+    float *saved_states;
+    void *workspace;
+    size_t workspace_bytes;
+} rdm_ssm_args;
+
+rdm_status rdm_ssm_fwd(const rdm_ssm_args *args, rdm_stream_t stream);
+
+/* Scratch bytes that let rdm_ssm_fwd cut sequences into segments (0 when it
+ * would not); (size_t)-1 on invalid arguments. */
+size_t rdm_ssm_fwd_workspace_size(const rdm_ssm_args *args);
+
+/* Bytes of `saved_states` (B*H*ceil(T/16)*D*N*4); 0 on invalid sizes. */
+size_t rdm_ssm_saved_states_size(int B, int H, int T, int D, int N);
+
+/* Reverse mode of rdm_ssm_fwd for dL/dy = grad_y, dL/dST = grad_ST (NULL =
+ * zero) and dL/d(conv_state_out) = grad_conv_state_out (NULL = zero).
+ *   fwd          : the forward's arguments (y, ST, conv_state_out unused);
+ *                  saved_states as the forward wrote them for the same
+ *                  arguments, or NULL to run it again into the workspace;
+ *                  workspace of at least rdm_ssm_bwd_workspace_size() bytes.
+ *   grad_x, grad_dt : [B,H,T,D] dtype, grad_B, grad_C : [B,G,T,N] dtype, grad_A :
+ *                  [H,D,N] float32, written; grad_z : [B,H,T,D] dtype, needed
+ *                  exactly when z is given
+ *   grad_dt_bias, grad_feedthrough [H,D], grad_conv_weight [H,D,W],
+ *   grad_conv_bias [H,D] float32, grad_S0 [B,H,D,N] float32,
+ *   grad_conv_state_in [B,H,W-1,D] dtype : written; NULL = skip
+ * Rows of the sequence gradients at and behind a sequence's length are written
+ * with zeros.  Sums over batch, tokens and heads are taken in a fixed order
+ * (no atomics). */
+typedef struct {
+    rdm_ssm_args fwd;
+    const void *grad_y;
+    const float *grad_ST;
+    const void *grad_conv_state_out;
+    void *grad_x, *grad_dt, *grad_z, *grad_B, *grad_C;
+    float *grad_A, *grad_dt_bias, *grad_feedthrough, *grad_conv_weight, *grad_conv_bias;
+    float *grad_S0;
+    void *grad_conv_state_in;
+} rdm_ssm_bwd_args;
+
+rdm_status rdm_ssm_bwd(const rdm_ssm_bwd_args *args, rdm_stream_t stream);
+
+/* Scratch bytes rdm_ssm_bwd needs (depends on whether saved_states is given);
+ * (size_t)-1 on invalid arguments. */
+size_t rdm_ssm_bwd_workspace_size(const rdm_ssm_bwd_args *args);
+
+/* One token: the same formulas with x, dt, z, y [B,H,D], Bm, Cm [B,G,N], the
+ * state S [B,H,D,N] float32 and conv_state [B,H,W-1,D] dtype (given exactly
+ * when W > 1) read and updated in place. */
+typedef struct {
+    int B, H, G, D, N, W;
+    rdm_dtype dtype;
+    rdm_gate_inputs gate_inputs;
+    int conv_silu;
+    const void *x, *dt, *Bm, *Cm, *z;
+    const float *A, *dt_bias, *feedthrough, *conv_weight, *conv_bias;
+    float *S;
+    void *conv_state;
+    void *y;
+} rdm_ssm_step_args;
+
+rdm_status rdm_ssm_step(const rdm_ssm_step_args *args, rdm_stream_t stream);
+
 /* ------------------------------------------------------------------ status */
 
 /* Synchronises `stream`, then reports (and clears) the device status word of
