@@ -100,6 +100,22 @@ class SsmStepArgs(ctypes.Structure):
                 ("conv_bias", _VP), ("S", _VP), ("conv_state", _VP), ("y", _VP)]
 
 
+class SkaQ8Cache(ctypes.Structure):
+    _fields_ = [("B", _I), ("H", _I), ("dk", _I), ("dv", _I), ("window", _I), ("block", _I), ("type", _I),
+                ("k", _VP), ("v", _VP), ("k_scale", _VP), ("v_scale", _VP), ("k_tail", _VP), ("v_tail", _VP),
+                ("pos", _VP)]
+
+
+class SkaQ8FillArgs(ctypes.Structure):
+    _fields_ = [("cache", SkaQ8Cache), ("T", _I), ("dtype", _I), ("k", _VP), ("v", _VP), ("lengths", _VP)]
+
+
+class SkaQ8DecodeArgs(ctypes.Structure):
+    _fields_ = [("cache", SkaQ8Cache), ("scale", ctypes.c_float), ("dtype", _I), ("q", _VP), ("k", _VP),
+                ("v", _VP), ("o", _VP), ("advance_pos", _I), ("workspace", _VP),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 class RdmError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -114,7 +130,8 @@ EXPORTS = ["rdm_ddts_fwd", "rdm_ddts_fwd_workspace_size", "rdm_ddts_saved_states
            "rdm_status_string", "rdm_ddts_set_test_hooks", "rdm_ddts_version", "rdm_shortconv_fwd",
            "rdm_shortconv_bwd", "rdm_shortconv_fwd_many", "rdm_shortconv_bwd_many", "rdm_ska_fwd",
            "rdm_ska_decode", "rdm_ssm_fwd", "rdm_ssm_fwd_workspace_size", "rdm_ssm_saved_states_size",
-           "rdm_ssm_bwd", "rdm_ssm_bwd_workspace_size", "rdm_ssm_step"]
+           "rdm_ssm_bwd", "rdm_ssm_bwd_workspace_size", "rdm_ssm_step", "rdm_ska_q8_fill",
+           "rdm_ska_q8_decode", "rdm_ska_q8_decode_workspace_size"]
 
 
 def load():
@@ -167,6 +184,12 @@ def load():
         lib.rdm_ssm_saved_states_size.restype = ctypes.c_size_t
         lib.rdm_ssm_step.argtypes = [ctypes.POINTER(SsmStepArgs), _VP]
         lib.rdm_ssm_step.restype = _I
+        lib.rdm_ska_q8_fill.argtypes = [ctypes.POINTER(SkaQ8FillArgs), _VP]
+        lib.rdm_ska_q8_fill.restype = _I
+        lib.rdm_ska_q8_decode.argtypes = [ctypes.POINTER(SkaQ8DecodeArgs), _VP]
+        lib.rdm_ska_q8_decode.restype = _I
+        lib.rdm_ska_q8_decode_workspace_size.argtypes = [ctypes.POINTER(SkaQ8DecodeArgs)]
+        lib.rdm_ska_q8_decode_workspace_size.restype = ctypes.c_size_t
         lib.rdm_ddts_set_test_hooks.argtypes = [ctypes.c_longlong, _I]
         lib.rdm_ddts_set_test_hooks.restype = _I
         lib.rdm_ddts_version.argtypes = []
@@ -577,7 +600,7 @@ def _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_b
     return a
 
 
-def _ssm_size(fn, a, where) -> int:
+def _size(fn, a, where) -> int:
     n = fn(ctypes.byref(a))
     if n == ctypes.c_size_t(-1).value:
         raise RdmError(RDM_ERR_INVALID_ARG, where)
@@ -598,7 +621,7 @@ def rdm_ssm_saved_states(x, A):
 def rdm_ssm_fwd_workspace_size(x, dt, A, Bm, Cm, *, conv_weight=None, gates="preact") -> int:
     a = _ssm_args(x, dt, A, Bm, Cm, None, None, None, None, conv_weight, None, None, True, None, gates,
                   None, None, None, None)
-    return _ssm_size(load().rdm_ssm_fwd_workspace_size, a, "rdm_ssm_fwd_workspace_size")
+    return _size(load().rdm_ssm_fwd_workspace_size, a, "rdm_ssm_fwd_workspace_size")
 
 
 def rdm_ssm_fwd(x, dt, A, Bm, Cm, *, S0=None, z=None, dt_bias=None, feedthrough=None, conv_weight=None,
@@ -625,7 +648,7 @@ def rdm_ssm_fwd(x, dt, A, Bm, Cm, *, S0=None, z=None, dt_bias=None, feedthrough=
         a = _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
                       conv_silu, lengths, gates, y, ST, conv_state_out, saved_states)
         if workspace is None:
-            need = _ssm_size(load().rdm_ssm_fwd_workspace_size, a, "rdm_ssm_fwd")
+            need = _size(load().rdm_ssm_fwd_workspace_size, a, "rdm_ssm_fwd")
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
         if workspace is not None and workspace is not False:
             a.workspace, a.workspace_bytes = _buffer(workspace, "workspace", x.device)
@@ -653,7 +676,7 @@ def _ssm_bwd_args(a, grad_y, grad_ST, grad_conv_state_out, g, dev):
 def rdm_ssm_bwd_workspace_size(x, dt, A, Bm, Cm, saved_states=None, *, conv_weight=None, gates="preact") -> int:
     a = _ssm_args(x, dt, A, Bm, Cm, None, None, None, None, conv_weight, None, None, True, None, gates,
                   None, None, None, saved_states)
-    return _ssm_size(load().rdm_ssm_bwd_workspace_size, SsmBwdArgs(a), "rdm_ssm_bwd_workspace_size")
+    return _size(load().rdm_ssm_bwd_workspace_size, SsmBwdArgs(a), "rdm_ssm_bwd_workspace_size")
 
 
 def rdm_ssm_bwd(x, dt, A, Bm, Cm, grad_y, grad_ST=None, grad_conv_state_out=None, *, S0=None, z=None,
@@ -681,7 +704,7 @@ def rdm_ssm_bwd(x, dt, A, Bm, Cm, grad_y, grad_ST=None, grad_conv_state_out=None
             raise TypeError("grad_y: expected a torch.Tensor")
         ba = _ssm_bwd_args(a, grad_y, grad_ST, grad_conv_state_out, g, x.device)
         if workspace is None:
-            need = _ssm_size(load().rdm_ssm_bwd_workspace_size, ba, "rdm_ssm_bwd")
+            need = _size(load().rdm_ssm_bwd_workspace_size, ba, "rdm_ssm_bwd")
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
         if workspace is not None:
             ba.fwd.workspace, ba.fwd.workspace_bytes = _buffer(workspace, "workspace", x.device)
@@ -717,6 +740,90 @@ def rdm_ssm_step(x, dt, A, Bm, Cm, S, *, z=None, dt_bias=None, feedthrough=None,
                         _arg(y, "y", (B, H, D), ty, dev))
         _check(load().rdm_ssm_step(ctypes.byref(a), _stream(stream)), "rdm_ssm_step")
     return y
+
+
+# ---------------------------------------------------------------- SW-SKA, 8-bit cache
+_CACHE_TYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
+
+
+def rdm_ska_q8_cache(B, H, dk, dv, window, *, block=64, dtype=torch.float8_e4m3fn, device="cuda"):
+    """Tensors of an empty 8-bit ring cache, in the order in which
+    rdm_ska_q8_fill and rdm_ska_q8_decode take them: k_cache, v_cache (codes,
+    torch.float8_e4m3fn or torch.int8), k_scale, v_scale, k_tail, v_tail, pos."""
+    if dtype not in _CACHE_TYPES:
+        raise TypeError(f"unsupported cache dtype {dtype} (float8_e4m3fn or int8)")
+    nb = (window + block - 1) // block
+    at = dict(device=device)
+    return (torch.zeros(B, window, dk, dtype=torch.uint8, **at).view(dtype),
+            torch.zeros(B, H, window, dv, dtype=torch.uint8, **at).view(dtype),
+            torch.ones(B, nb, **at), torch.ones(B, H, nb, **at),
+            torch.zeros(B, block, dk, dtype=torch.bfloat16, **at),
+            torch.zeros(B, H, block, dv, dtype=torch.bfloat16, **at),
+            torch.zeros(B, dtype=torch.int32, **at))
+
+
+def _q8_cache(B, H, dk, dv, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, dev):
+    ty = k_cache.dtype
+    if ty not in _CACHE_TYPES:
+        raise TypeError(f"unsupported cache dtype {ty} (float8_e4m3fn or int8)")
+    if k_cache.dim() != 3 or k_tail.dim() != 3 or k_tail.shape[1] < 1:
+        raise ValueError("k_cache: expected [B,window,dk], k_tail: [B,block,dk]")
+    w, R = k_cache.shape[1], k_tail.shape[1]
+    nb, bf = (w + R - 1) // R, torch.bfloat16
+    return SkaQ8Cache(B, H, dk, dv, w, R, _CACHE_TYPES[ty], _arg(k_cache, "k_cache", (B, w, dk), ty, dev),
+                      _arg(v_cache, "v_cache", (B, H, w, dv), ty, dev), _arg(k_scale, "k_scale", (B, nb), _F32, dev),
+                      _arg(v_scale, "v_scale", (B, H, nb), _F32, dev), _arg(k_tail, "k_tail", (B, R, dk), bf, dev),
+                      _arg(v_tail, "v_tail", (B, H, R, dv), bf, dev), _arg(pos, "pos", (B,), torch.int32, dev))
+
+
+def rdm_ska_q8_fill(k, v, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, *, lengths=None, stream=None):
+    """Fills an 8-bit ring cache (rdm_ska_q8_cache) from a prompt's keys
+    [B,T,dk] and values [B,H,T,dv] in bf16, as so many decode steps would, and
+    sets pos; lengths [B] int32: tokens of each sequence."""
+    dev = _current(k)
+    if k.dim() != 3 or v.dim() != 4:
+        raise ValueError("k: expected [B,T,dk], v: [B,H,T,dv]")
+    B, T, dk = k.shape
+    H, dv = v.shape[1], v.shape[3]
+    a = SkaQ8FillArgs(_q8_cache(B, H, dk, dv, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, dev), T,
+                      _dtype_code(k), _arg(k, "k", (B, T, dk), k.dtype, dev), _arg(v, "v", (B, H, T, dv), k.dtype, dev),
+                      _arg(lengths, "lengths", (B,), torch.int32, dev))
+    _check(load().rdm_ska_q8_fill(ctypes.byref(a), _stream(stream)), "rdm_ska_q8_fill")
+
+
+def _q8_decode_args(q, k, v, cache, scale, o, advance_pos):
+    dev = _current(q)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q: expected [B,H,dk], v: [B,H,dv]")
+    B, H, dk = q.shape
+    dv, ty = v.shape[2], q.dtype
+    return SkaQ8DecodeArgs(_q8_cache(B, H, dk, dv, *cache, dev), float(scale), _dtype_code(q),
+                           _arg(q, "q", (B, H, dk), ty, dev), _arg(k, "k", (B, dk), ty, dev),
+                           _arg(v, "v", (B, H, dv), ty, dev), _arg(o, "o", (B, H, dv), ty, dev),
+                           int(bool(advance_pos)), None, 0)
+
+
+def rdm_ska_q8_decode_workspace_size(q, k, v, *cache) -> int:
+    a = _q8_decode_args(q, k, v, cache, 0.0, None, True)
+    return _size(load().rdm_ska_q8_decode_workspace_size, a, "rdm_ska_q8_decode_workspace_size")
+
+
+def rdm_ska_q8_decode(q, k, v, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, *, scale=0.0,
+                      advance_pos=True, o=None, workspace=None, stream=None):
+    """One SW-SKA decode step over an 8-bit ring cache (rdm_ska_q8_cache),
+    updated in place: q [B,H,dk], k [B,dk], v [B,H,dv] bf16.  scale 0 means
+    1/sqrt(dk); workspace=False runs without one.  Returns o [B,H,dv]."""
+    with _on(stream):
+        if o is None:
+            o = torch.empty_like(v)
+        a = _q8_decode_args(q, k, v, (k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos), scale, o, advance_pos)
+        if workspace is None:
+            need = _size(load().rdm_ska_q8_decode_workspace_size, a, "rdm_ska_q8_decode")
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        if workspace is not None and workspace is not False:
+            a.workspace, a.workspace_bytes = _buffer(workspace, "workspace", q.device)
+        _check(load().rdm_ska_q8_decode(ctypes.byref(a), _stream(stream)), "rdm_ska_q8_decode")
+    return o
 
 
 def rdm_ddts_sync_status(stream=None) -> int:

@@ -11,6 +11,7 @@
 #include "launch.h"
 #include "rdm_common.cuh"
 #include "ska_launch.h"
+#include "ska_q8_launch.h"
 #include "ssm_launch.h"
 
 namespace rdm {
@@ -463,6 +464,78 @@ rdm_status rdm_ska_decode(const rdm_ska_decode_args* a, rdm_stream_t stream) {
     p.err = status_word();
     if (!p.err) return RDM_ERR_CUDA;
     return from_cuda(launch_ska_decode(p, static_cast<cudaStream_t>(stream)));
+}
+
+static rdm_status ska_q8_check(const rdm_ska_q8_cache& c) {
+    if (c.B < 1 || c.H < 1 || c.window < 1) return RDM_ERR_INVALID_ARG;
+    if (c.type != RDM_CACHE_E4M3 && c.type != RDM_CACHE_INT8) return RDM_ERR_INVALID_ARG;
+    if (!ska_dim_ok(c.dk) || !ska_dim_ok(c.dv) || c.window > 32768) return RDM_ERR_UNSUPPORTED;
+    if (c.block != 16 && c.block != 32 && c.block != 64) return RDM_ERR_UNSUPPORTED;
+    if ((double)c.B * ((double)c.H + 1) * ((c.window + c.block - 1) / c.block) > 2.0e9) return RDM_ERR_INVALID_ARG;
+    const void* in[] = {c.k, c.v, c.k_scale, c.v_scale, c.k_tail, c.v_tail, c.pos};
+    for (int i = 0; i < 7; ++i)
+        if (!in[i] || (i < 6 ? !aligned(in[i]) : (reinterpret_cast<uintptr_t>(in[i]) & 3u) != 0))
+            return RDM_ERR_INVALID_ARG;
+    return RDM_OK;
+}
+
+static SkaQ8Cache ska_q8_cache(const rdm_ska_q8_cache& a) {
+    SkaQ8Cache c;
+    c.B = a.B; c.H = a.H; c.dk = a.dk; c.dv = a.dv; c.window = a.window; c.block = a.block;
+    c.int8 = a.type == RDM_CACHE_INT8;
+    c.k = static_cast<unsigned char*>(a.k); c.v = static_cast<unsigned char*>(a.v);
+    c.k_scale = a.k_scale; c.v_scale = a.v_scale; c.k_tail = a.k_tail; c.v_tail = a.v_tail; c.pos = a.pos;
+    return c;
+}
+
+rdm_status rdm_ska_q8_fill(const rdm_ska_q8_fill_args* a, rdm_stream_t stream) {
+    if (!a) return RDM_ERR_INVALID_ARG;
+    rdm_status st = ska_q8_check(a->cache);
+    if (st != RDM_OK) return st;
+    if (a->T < 0 || a->T > (1 << 30)) return RDM_ERR_INVALID_ARG;
+    if (a->dtype != RDM_BF16) return a->dtype == RDM_F32 ? RDM_ERR_UNSUPPORTED : RDM_ERR_INVALID_ARG;
+    if (a->T > 0 && (!a->k || !a->v)) return RDM_ERR_INVALID_ARG;
+    if (!opt_aligned(a->k) || !opt_aligned(a->v) || (reinterpret_cast<uintptr_t>(a->lengths) & 3u) != 0)
+        return RDM_ERR_INVALID_ARG;
+    SkaQ8FillParams p;
+    p.c = ska_q8_cache(a->cache);
+    p.T = a->T; p.k = a->k; p.v = a->v; p.lengths = a->lengths;
+    p.err = status_word();
+    if (!p.err) return RDM_ERR_CUDA;
+    return from_cuda(launch_ska_q8_fill(p, static_cast<cudaStream_t>(stream)));
+}
+
+static SkaQ8DecodeParams ska_q8_decode_params(const rdm_ska_q8_decode_args* a) {
+    SkaQ8DecodeParams p;
+    memset(&p, 0, sizeof(p));
+    p.c = ska_q8_cache(a->cache);
+    p.scale = ska_scale(a->scale, a->cache.dk);
+    p.q = a->q; p.k = a->k; p.v = a->v; p.o = a->o;
+    p.advance = a->advance_pos != 0;
+    p.ws = a->workspace;
+    p.ws_bytes = a->workspace ? a->workspace_bytes : 0;
+    return p;
+}
+
+size_t rdm_ska_q8_decode_workspace_size(const rdm_ska_q8_decode_args* a) {
+    if (!a || ska_q8_check(a->cache) != RDM_OK) return (size_t)-1;
+    return ska_q8_decode_workspace(ska_q8_decode_params(a));
+}
+
+rdm_status rdm_ska_q8_decode(const rdm_ska_q8_decode_args* a, rdm_stream_t stream) {
+    if (!a) return RDM_ERR_INVALID_ARG;
+    rdm_status st = ska_q8_check(a->cache);
+    if (st != RDM_OK) return st;
+    if (!(a->scale >= 0.0f) || isinf(a->scale)) return RDM_ERR_INVALID_ARG;
+    if (a->dtype != RDM_BF16) return a->dtype == RDM_F32 ? RDM_ERR_UNSUPPORTED : RDM_ERR_INVALID_ARG;
+    const void* in[] = {a->q, a->k, a->v, a->o};
+    for (const void* p : in)
+        if (!p || !aligned(p)) return RDM_ERR_INVALID_ARG;
+    if (!opt_aligned(a->workspace)) return RDM_ERR_INVALID_ARG;
+    SkaQ8DecodeParams p = ska_q8_decode_params(a);
+    p.err = status_word();
+    if (!p.err) return RDM_ERR_CUDA;
+    return from_cuda(launch_ska_q8_decode(p, static_cast<cudaStream_t>(stream)));
 }
 
 static bool ssm_dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }

@@ -414,6 +414,86 @@ typedef struct {
 
 rdm_status rdm_ska_decode(const rdm_ska_decode_args *args, rdm_stream_t stream);
 
+/* ------------------------------------------------------- SW-SKA, 8-bit cache
+ * The decode step of the sliding-window shared-key attention over ring caches
+ * held in 8 bits, with a scale for each block of slots and head (the shared
+ * key has one row of scales).  Half the bytes of the bf16 rings, which are
+ * nearly all that a decode step reads.
+ *
+ *   k       : [B,window,d_k] codes       v       : [B,H,window,d_v] codes
+ *   k_scale : [B,NB] float32             v_scale : [B,H,NB] float32
+ *   k_tail  : [B,block,d_k] bf16         v_tail  : [B,H,block,d_v] bf16
+ *   pos     : [B] int32 tokens of each sequence seen so far
+ *   block in {16, 32, 64}; NB = ceil(window/block), the last block may be short;
+ *   window <= 32768; d_k, d_v in {64, 128}.
+ * The token at position p lives in slot p mod window.  The tokens of the block
+ * being written are kept in bf16 in the tail (row i: slot i of the block), used
+ * from there, and rounded once when the block is full; slots of that block that
+ * the tail has not reached still hold the round before.  So every token is
+ * rounded at most once, and a prompt leaves the same cache as its tokens one by
+ * one.  Slots never written are never read.
+ *
+ *   RDM_CACHE_E4M3: value = scale * code, scale the least power of two (2^-126
+ *     at least) with the block's largest magnitude within 448 * scale.
+ *   RDM_CACHE_INT8: value = scale * code, scale the largest magnitude / 127,
+ *     codes -127 .. 127 by rounding value / scale to nearest even.
+ *   A block of zeros has the scale 1.  Keys and values are meant to be finite:
+ *   others do not count for the scale; infinities take the largest code, NaN
+ *   stays NaN in e4m3 and becomes 0 in int8.  Decoding uses any scales it finds.
+ */
+typedef enum { RDM_CACHE_E4M3 = 0, RDM_CACHE_INT8 = 1 } rdm_cache_type;
+
+typedef struct {
+    int B, H, dk, dv, window, block;
+    rdm_cache_type type;
+    void *k, *v;
+    float *k_scale, *v_scale;
+    void *k_tail, *v_tail;
+    int *pos;
+} rdm_ska_q8_cache;
+
+/* Fills the caches from a prompt: k [B,T,d_k], v [B,H,T,d_v] bf16, lengths [B]
+ * int32 (0..T tokens of each sequence) or NULL for T each.  Leaves the cache of
+ * T (or lengths[b]) decode steps from pos = 0, and sets pos; blocks that no token
+ * reached and tail rows without a token of the unfinished block are left as they
+ * were.  A length out of range counts as the nearest end and makes rdm_ddts_sync_status return
+ * RDM_ERR_INVALID_ARG.  dtype must be RDM_BF16. */
+typedef struct {
+    rdm_ska_q8_cache cache;
+    int T;
+    rdm_dtype dtype;
+    const void *k, *v;
+    const int *lengths;
+} rdm_ska_q8_fill_args;
+
+rdm_status rdm_ska_q8_fill(const rdm_ska_q8_fill_args *args, rdm_stream_t stream);
+
+/* One token per sequence, as rdm_ska_decode: the new key and value enter the
+ * cache at pos[b], o attends to the last min(pos+1, window) tokens, pos[b] += 1
+ * when advance_pos != 0.  A negative pos[b] leaves that sequence untouched and
+ * makes rdm_ddts_sync_status return RDM_ERR_INVALID_ARG.  pos[b] must stay
+ * below 2^31 - 1.
+ *   workspace : optional scratch; with rdm_ska_q8_decode_workspace_size() bytes
+ *               long windows of few sequences are split over several CTAs.
+ *               Contents on entry are ignored; calls whose kernels may overlap
+ *               (graphs that may run at once, too) must not share it. */
+typedef struct {
+    rdm_ska_q8_cache cache;
+    float scale;                 /* > 0, or 0 for 1/sqrt(d_k) */
+    rdm_dtype dtype;
+    const void *q, *k, *v;       /* [B,H,d_k], [B,d_k], [B,H,d_v] bf16 */
+    void *o;                     /* [B,H,d_v] bf16 */
+    int advance_pos;
+    void *workspace;
+    size_t workspace_bytes;
+} rdm_ska_q8_decode_args;
+
+rdm_status rdm_ska_q8_decode(const rdm_ska_q8_decode_args *args, rdm_stream_t stream);
+
+/* Scratch bytes that let rdm_ska_q8_decode split windows (0 when it would not);
+ * (size_t)-1 on invalid arguments. */
+size_t rdm_ska_q8_decode_workspace_size(const rdm_ska_q8_decode_args *args);
+
 /* ------------------------------------------------------- selective scan
  * Selective state space scan with its short causal convolution (Gu and Dao,
  * "Mamba: Linear-Time Sequence Modeling with Selective State Spaces", arXiv
