@@ -54,20 +54,13 @@ __device__ __forceinline__ unsigned char encode(float x, float scale, float inv)
     return __nv_cvt_float_to_fp8(x * inv, __NV_SATFINITE, __NV_E4M3);
 }
 
-template <bool I8>
-__device__ __forceinline__ float decode8(unsigned char c) {
-    if (I8) return (float)(signed char)c;
-    __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-    return __half2float(__half(h));
-}
-
 constexpr int kThreads = 128;
 
 // Rounds `rows` rows of D values (row r at src + r * D) into dst and *scale, by
-// the whole CTA of kThreads.
+// the whole CTA.
 template <bool I8, int D>
 __device__ void round_block(const __nv_bfloat16* src, int rows, unsigned char* dst, float* scale) {
-    __shared__ float red[kThreads / 32];
+    __shared__ float red[32];
     const int n8 = rows * (D / 8);
     float most = 0.0f;
     for (int i = threadIdx.x; i < n8; i += blockDim.x) {
@@ -143,90 +136,388 @@ __global__ void __launch_bounds__(kThreads) ska_q8_fill_kernel(const SkaQ8FillPa
 }
 
 // ------------------------------------------------------------------ one token
-// One CTA per (b, h).  First version: scores of all slots in shared memory.
+// A CTA of eight warps takes a group of up to eight heads of one sequence and a
+// range of its slots, 512 at a time:
+//   scores  16 slots a warp, mma (slots x d_k) (d_k x 8 heads), the shared key rows
+//           read once for the group's heads; into shared memory
+//   weights a warp (or 8 / heads of them) per head: running maxima and sum, then
+//           2^(s + log2 v_scale - m') as two f16 halves: the block's scale is part
+//           of the exponent, so blocks of any scale meet in one accumulator
+//   values  mma (d_v x 16 slots) (16 slots x the weight's halves), the codes turned
+//           into f16 pairs in registers (exact: e4m3 and int8 both fit f16's 11 bits)
+// Without the tensor cores the conversions and products of the values alone would
+// cost about 70 of an SM's 128 lane operations a clock at the memory's rate; with
+// them each byte of V costs 0.25 byte permutations, half a conversion and 1/256 of
+// an mma a warp, and the sweep stays bound by HBM.
+// The tail's slots go through the same steps in bf16, the weights in three parts.
+constexpr int kWarps = 8, kDecThreads = 32 * kWarps, kChunk = 512, kStride = kChunk + 4;
+
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four codes as two f16 pairs.
+template <bool I8>
+__device__ __forceinline__ uint2 f16_pairs(uint32_t w) {
+    if (I8) {  // 0x6400 | (code + 128) is 1024 + code + 128 in f16
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+        uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+        __half2 a = __hsub2(*reinterpret_cast<__half2*>(&lo), off), b = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
+        return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+    }
+    uint2 r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(r.x), "=r"(r.y) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Heads of a group, groups, splits of the window and slots of each.
+struct Q8Plan {
+    int G, groups, splits, range;
+    int cluster;   // the groups of a sequence form a cluster, and pos is advanced in the kernel
+    float *m, *l, *o;  // partial results [B,H,splits], [B,H,splits], [B,H,splits,dv]
+};
+
 template <bool I8, int DK, int DV>
-__global__ void __launch_bounds__(kThreads) ska_q8_decode_kernel(const SkaQ8DecodeParams p) {
-    extern __shared__ float sc[];  // [window]
-    __shared__ float qs[DK];
-    __shared__ float red[kThreads / 32];
-    __shared__ float part[kThreads / (DV / 8)][DV];
+__global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const SkaQ8DecodeParams p, const Q8Plan pl) {
+    constexpr int KW = DK / 16;    // words of codes a lane has of a key row
+    constexpr int VB = DV / 8;     // value columns a lane has
+    constexpr int MT = DV / 16;    // value tiles of 16 columns
+    __shared__ __align__(16) float sc[kWarps][kStride];
+    __shared__ __align__(16) __half wt[kWarps][2][kChunk];
+    __shared__ __align__(16) __nv_bfloat16 qs[kWarps][DK];
+    __shared__ float part[kWarps][DV];
+    __shared__ float stat[kWarps][3];
     const SkaQ8Cache& c = p.c;
-    const int b = blockIdx.x / c.H, h = blockIdx.x % c.H, tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, l4 = lane & 3;
+    const int group = blockIdx.x % pl.groups, b = blockIdx.x / pl.groups, split = blockIdx.y;
+    const int h0 = group * pl.G, nh = min(pl.G, c.H - h0);
     const int pos = c.pos[b];
-    if (pos < 0) {
-        if (tid == 0) atomicOr(p.err, kErrBadValue);
-        return;
-    }
-    const int w = c.window, R = c.block, nb = (w + R - 1) / R;
-    const int n = pos < w ? pos + 1 : w, cur = pos % w, at = cur / R * R, fill = cur - at;
-    const size_t bh = (size_t)b * c.H + h;
+    if (pl.cluster) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // pos is read
+    const int w = c.window, R = c.block, nb = (w + R - 1) / R, rs = 31 - __clz(R);
+    const int n = pos < 0 ? 0 : pos < w ? pos + 1 : w;
+    const int cur = pos < 0 ? 0 : pos % w, at = cur & ~(R - 1), fill = cur - at;
+    const int s0 = split * pl.range, s1 = min(s0 + pl.range, n);
+    const bool tail_here = pos >= 0 && at >= s0 && at < s0 + pl.range;
+    if (pos < 0 && tid == 0) atomicOr(p.err, kErrBadValue);
+    const size_t bh0 = (size_t)b * c.H + h0;
     const __nv_bfloat16* kin = static_cast<const __nv_bfloat16*>(p.k) + (size_t)b * DK;
-    const __nv_bfloat16* vin = static_cast<const __nv_bfloat16*>(p.v) + bh * DV;
+    const __nv_bfloat16* vin = static_cast<const __nv_bfloat16*>(p.v) + bh0 * DV;
     __nv_bfloat16* kt = static_cast<__nv_bfloat16*>(c.k_tail) + (size_t)b * R * DK;
-    __nv_bfloat16* vt = static_cast<__nv_bfloat16*>(c.v_tail) + bh * R * DV;
-    if (h == 0 && tid < DK) kt[(size_t)fill * DK + tid] = kin[tid];
-    if (tid < DV) vt[(size_t)fill * DV + tid] = vin[tid];
-    if (tid < DK) qs[tid] = __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[bh * DK + tid]) * p.scale * kLog2e;
-    __syncthreads();
-    float mx = -INFINITY;
-    for (int u = tid; u < n; u += kThreads) {
-        float a = 0.0f;
-        if (u >= at && u <= cur) {  // from the tail; the new key from the inputs
-            const __nv_bfloat16* r = u == cur ? kin : kt + (size_t)(u - at) * DK;
-            for (int i = 0; i < DK; ++i) a = fmaf(qs[i], __bfloat162float(r[i]), a);
-        } else {
-            const unsigned char* r = c.k + ((size_t)b * w + u) * DK;
-            for (int i = 0; i < DK; ++i) a = fmaf(qs[i], decode8<I8>(r[i]), a);
-            a *= c.k_scale[(size_t)b * nb + u / R];
-        }
-        sc[u] = a;
-        mx = fmaxf(mx, a);
-    }
+    __nv_bfloat16* vt = static_cast<__nv_bfloat16*>(c.v_tail) + bh0 * R * DV;
+    const unsigned char* kc = c.k + (size_t)b * w * DK;
+
+    // this warp's head: several warps share one where there are few
+    const int wph = kWarps / nh, hd = min(warp / wph, nh - 1), sub = warp % wph;
+    const bool busy = warp < wph * nh;
+    const unsigned char* vc = c.v + (bh0 + hd) * w * DV;
+    const float* vsc = c.v_scale + (bh0 + hd) * nb;
+    float m = -INFINITY, m2 = -3e38f, l = 0.0f;  // m of the scores, m2 with the scales in them
+    float acc[MT][4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    __syncthreads();
-    float sum = 0.0f;
-    for (int u = tid; u < n; u += kThreads) {
-        const float e = ex2_fast(sc[u] - mx);
-        sc[u] = e;
-        sum += e;
-    }
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((tid & 31) == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    sum = red[0] + red[1] + red[2] + red[3];
-    constexpr int XP = DV / 8, LG = kThreads / XP;
-    const int x = tid % XP, lg = tid / XP;
-    float acc[8] = {};
-    for (int u = lg; u < n; u += LG) {
-        const float pu = sc[u];
-        if (u >= at && u <= cur) {
-            const __nv_bfloat16* r = vt + (size_t)(u - at) * DV + 8 * x;
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(pu, __bfloat162float(r[e]), acc[e]);
-        } else {
-            const unsigned char* r = c.v + (bh * w + u) * DV + 8 * x;
-            const float ps = pu * c.v_scale[bh * nb + u / R];
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(ps, decode8<I8>(r[e]), acc[e]);
+        for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
+
+    if (s0 < s1) {
+        // queries: as they are for the tail, and as f16 for the codes, each head's
+        // times a power of two that puts its largest near 2^14 (exact)
+        for (int i = tid; i < kWarps * DK / 8; i += kDecThreads) {
+            const int hh = i / (DK / 8), x = i % (DK / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (hh < nh) v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (bh0 + hh) * DK)[x];
+            reinterpret_cast<uint4*>(qs[hh])[x] = v;
         }
-    }
-    for (int e = 0; e < 8; ++e) part[lg][8 * x + e] = acc[e];
-    __syncthreads();
-    if (tid < DV) {
-        float a = 0.0f;
-        for (int l = 0; l < LG; ++l) a += part[l][tid];
-        static_cast<__nv_bfloat16*>(p.o)[bh * DV + tid] = __float2bfloat16_rn(a / sum);
-    }
-    if (cur == w - 1 || fill == R - 1) {  // the block is full (its slots are read from the tail in this step)
-        if (h == 0) {
+        __syncthreads();
+        // lane's dimensions of a row: 16 l4 .. + 15, and 64 more on for d_k = 128; heads by g
+        uint32_t qf[KW][2];
+        float qmul;
+        {
+            float most = 0.0f;
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+                const int d = (j >> 2) * 64 + l4 * 16 + (j & 3) * 4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) most = fmaxf(most, finite_abs(__bfloat162float(qs[g][d + e])));
+            }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            int e2 = most > 0.0f ? (int)(__float_as_uint(most) >> 23) - 127 - 14 : 0;  // most in 2^(e2+14) .. 2^(e2+15)
+            e2 = max(-126, e2);
+            const float inv = __uint_as_float((unsigned)(127 - e2) << 23);
+            qmul = __uint_as_float((unsigned)(127 + e2) << 23) * (p.scale * kLog2e);
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+                const int d = (j >> 2) * 64 + l4 * 16 + (j & 3) * 4;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    __half2 hv = __floats2half2_rn(__bfloat162float(qs[g][d + 2 * e]) * inv, __bfloat162float(qs[g][d + 2 * e + 1]) * inv);
+                    qf[j][e] = *reinterpret_cast<uint32_t*>(&hv);
+                }
+            }
+        }
+        // multipliers of the two heads whose scores this lane gets from an mma
+        const float qm0 = __shfl_sync(0xffffffffu, qmul, 8 * l4), qm1 = __shfl_sync(0xffffffffu, qmul, 8 * l4 + 4);
+
+        for (int c0 = s0; c0 < s1; c0 += kChunk) {
+            const int c1 = min(c0 + kChunk, s1);
+            // ---- scores
+            for (int t0 = c0 + 16 * warp; t0 < c1; t0 += 16 * kWarps) {
+                const int lo = (t0 & ~(R - 1)) == at ? max(t0, cur + 1) : t0, hi = min(t0 + 16, n);
+                if (lo >= hi) continue;  // all of them in the tail
+                const float ks = c.k_scale[(size_t)b * nb + (t0 >> rs)];
+                uint32_t ka[2][KW];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {  // rows without a token of the cache repeat one that has
+                    const int u = min(max(t0 + g + 8 * r, lo), hi - 1);
+                    const uint4* row = reinterpret_cast<const uint4*>(kc + (size_t)u * DK);
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x) {
+                        const uint4 v = row[4 * x + l4];
+                        ka[r][4 * x] = v.x; ka[r][4 * x + 1] = v.y; ka[r][4 * x + 2] = v.z; ka[r][4 * x + 3] = v.w;
+                    }
+                }
+                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < KW; ++j) {
+                    const uint2 x = f16_pairs<I8>(ka[0][j]), y = f16_pairs<I8>(ka[1][j]);
+                    const uint32_t a[4] = {x.x, y.x, x.y, y.y};
+                    mma_f16(s, a, qf[j][0], qf[j][1]);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int u = t0 + g + 8 * r;
+                    if (u < lo || u >= hi) continue;
+                    sc[2 * l4][u - c0] = s[2 * r] * (ks * qm0);
+                    sc[2 * l4 + 1][u - c0] = s[2 * r + 1] * (ks * qm1);
+                }
+            }
+            const bool tail_now = tail_here && at >= c0 && at < c0 + kChunk;
+            if (tail_now)
+                for (int t0 = 16 * warp; t0 <= fill; t0 += 16 * kWarps) {
+                    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const __nv_bfloat16* row[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int i = min(t0 + g + 8 * r, fill);
+                        row[r] = i == fill ? kin : kt + (size_t)i * DK;
+                    }
+#pragma unroll
+                    for (int j = 0; j < KW; ++j) {
+                        const int d = (j >> 2) * 64 + l4 * 16 + (j & 3) * 4;
+                        const uint2 x = *reinterpret_cast<const uint2*>(row[0] + d), y = *reinterpret_cast<const uint2*>(row[1] + d);
+                        const uint2 qv = *reinterpret_cast<const uint2*>(&qs[g][d]);
+                        const uint32_t a[4] = {x.x, y.x, x.y, y.y};
+                        mma_bf16(s, a, qv.x, qv.y);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int i = t0 + g + 8 * r;
+                        if (i > fill) continue;
+                        sc[2 * l4][at - c0 + i] = s[2 * r] * (p.scale * kLog2e);
+                        sc[2 * l4 + 1][at - c0 + i] = s[2 * r + 1] * (p.scale * kLog2e);
+                    }
+                }
             __syncthreads();
-            round_block<I8, DK>(kt, fill + 1, c.k + ((size_t)b * w + at) * DK, c.k_scale + (size_t)b * nb + at / R);
+            // ---- weights of this warp's head, and its values
+            if (busy) {
+                float cm = -INFINITY, cm2 = -3e38f;
+                for (int u = c0 + lane; u < c1; u += 32) {
+                    const float s = sc[hd][u - c0];
+                    const bool tl = u >= at && u <= cur;
+                    cm = fmaxf(cm, s);
+                    cm2 = fmaxf(cm2, tl ? s : s + __log2f(vsc[u >> rs]));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
+                    cm2 = fmaxf(cm2, __shfl_xor_sync(0xffffffffu, cm2, o));
+                }
+                const float nm = fmaxf(m, cm), nm2 = fmaxf(m2, cm2);
+                const float f2 = ex2_fast(m2 - nm2);
+                l *= m == nm ? 1.0f : ex2_fast(m - nm);
+                m = nm;
+                m2 = nm2;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][e] *= f2;
+                const int tiles = (c1 - c0 + 15) / 16;
+                for (int i = lane; i < ((tiles - sub + wph - 1) / wph) * 16; i += 32) {
+                    const int x = 16 * (sub + wph * (i >> 4)) + (i & 15), u = c0 + x;
+                    float e = 0.0f;
+                    if (u < c1) {
+                        const float s = sc[hd][x];
+                        l += ex2_fast(s - m);
+                        if (u < at || u > cur) e = ex2_fast(s + __log2f(vsc[u >> rs]) - m2);
+                    }
+                    const __half hi = __float2half_rn(e);
+                    wt[warp][0][i] = hi;
+                    wt[warp][1][i] = __float2half_rn(e - __half2float(hi));
+                }
+                __syncwarp();
+                int k = 0;
+#pragma unroll 2
+                for (int tt = sub; tt < tiles; tt += wph, ++k) {
+                    const int t0 = c0 + 16 * tt;
+                    const int lo = (t0 & ~(R - 1)) == at ? max(t0, cur + 1) : t0, hi = min(t0 + 16, c1);
+                    if (lo >= hi) continue;
+                    uint32_t v[4][VB / 4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {  // tokens 2 l4, 2 l4 + 1, and 8 on
+                        const int u = min(max(t0 + 2 * l4 + (r & 1) + 4 * (r & 2), lo), hi - 1);
+                        const unsigned char* row = vc + (size_t)u * DV + VB * g;
+                        if (VB == 16) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(row);
+                            v[r][0] = x.x; v[r][1] = x.y; v[r][VB / 4 - 2] = x.z; v[r][VB / 4 - 1] = x.w;
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2*>(row);
+                            v[r][0] = x.x; v[r][1] = x.y;
+                        }
+                    }
+                    uint32_t b0 = 0, b1 = 0;
+                    if (g < 2) {
+                        b0 = *reinterpret_cast<const uint32_t*>(&wt[warp][g][16 * k + 2 * l4]);
+                        b1 = *reinterpret_cast<const uint32_t*>(&wt[warp][g][16 * k + 2 * l4 + 8]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {  // columns VB g + 2 i and + 1
+                        const unsigned sel = i & 1 ? 0x7362u : 0x5140u;
+                        const uint2 x = f16_pairs<I8>(__byte_perm(v[0][i >> 1], v[1][i >> 1], sel));
+                        const uint2 y = f16_pairs<I8>(__byte_perm(v[2][i >> 1], v[3][i >> 1], sel));
+                        const uint32_t a[4] = {x.x, x.y, y.x, y.y};
+                        mma_f16(acc[i], a, b0, b1);
+                    }
+                }
+                if (tail_now)
+                    for (int t0 = 16 * sub; t0 <= fill; t0 += 16 * wph) {
+                        const __nv_bfloat16* row[4];
+                        float e[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int i = t0 + 2 * l4 + (r & 1) + 4 * (r & 2), ic = min(i, fill);
+                            row[r] = (ic == fill ? vin + (size_t)hd * DV : vt + ((size_t)hd * R + ic) * DV) + VB * g;
+                            e[r] = i <= fill ? ex2_fast(sc[hd][at - c0 + ic] - m2) : 0.0f;
+                            for (int x = 0; x < g && x < 3; ++x) e[r] -= __bfloat162float(__float2bfloat16_rn(e[r]));
+                            if (g > 2) e[r] = 0.0f;
+                        }
+                        const uint32_t b0 = bf16_pair(e[0], e[1]), b1 = bf16_pair(e[2], e[3]);
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) v[r] = *reinterpret_cast<const uint32_t*>(row[r] + 2 * i);
+                            const uint32_t a[4] = {__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                                                   __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[2], v[3], 0x7632)};
+                            mma_bf16(acc[i], a, b0, b1);
+                        }
+                    }
+            }
+            __syncthreads();
         }
-        round_block<I8, DV>(vt, fill + 1, c.v + (bh * w + at) * DV, c.v_scale + bh * nb + at / R);
     }
+    // ---- join the halves and parts, then the warps of a head
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+        stat[warp][0] = m;
+        stat[warp][1] = m2;
+        stat[warp][2] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        float x = acc[i][0] + acc[i][1], y = acc[i][2] + acc[i][3];
+        x += __shfl_down_sync(0xffffffffu, x, 1);
+        y += __shfl_down_sync(0xffffffffu, y, 1);
+        if (l4 == 0) {
+            part[warp][VB * g + 2 * i] = x;
+            part[warp][VB * g + 2 * i + 1] = y;
+        }
+    }
+    __syncthreads();
+    if (pos >= 0)
+        for (int i = tid; i < nh * DV; i += kDecThreads) {
+            const int hh = i / DV, x = i % DV, w0 = hh * wph;
+            // the warps of a head saw the same scores, so their maxima agree
+            float a = 0.0f, sum = 0.0f;
+            for (int k = 0; k < wph; ++k) {
+                a += part[w0 + k][x];
+                sum += stat[w0 + k][2];
+            }
+            a *= ex2_fast(stat[w0][1] - stat[w0][0]);
+            const size_t bh = bh0 + hh;
+            if (pl.splits == 1) {
+                static_cast<__nv_bfloat16*>(p.o)[bh * DV + x] = __float2bfloat16_rn(a / sum);
+            } else {
+                const size_t at2 = bh * pl.splits + split;
+                if (s0 < s1) pl.o[at2 * DV + x] = a;
+                if (x == 0) {
+                    pl.m[at2] = s0 < s1 ? stat[w0][0] : -INFINITY;
+                    pl.l[at2] = sum;
+                }
+            }
+        }
+    // ---- the new token, and the block if it is full with it
+    if (tail_here) {
+        if (group == 0 && tid < DK / 8)
+            reinterpret_cast<uint4*>(kt + (size_t)fill * DK)[tid] = reinterpret_cast<const uint4*>(kin)[tid];
+        for (int i = tid; i < nh * (DV / 8); i += kDecThreads) {
+            const int hh = i / (DV / 8), x = i % (DV / 8);
+            reinterpret_cast<uint4*>(vt + ((size_t)hh * R + fill) * DV)[x] = reinterpret_cast<const uint4*>(vin + (size_t)hh * DV)[x];
+        }
+        if (cur == w - 1 || fill == R - 1) {
+            __syncthreads();
+            if (group == 0)
+                round_block<I8, DK>(kt, fill + 1, c.k + ((size_t)b * w + at) * DK, c.k_scale + (size_t)b * nb + at / R);
+            for (int hh = 0; hh < nh; ++hh)
+                round_block<I8, DV>(vt + (size_t)hh * R * DV, fill + 1, c.v + ((bh0 + hh) * w + at) * DV,
+                                    c.v_scale + (bh0 + hh) * nb + at / R);
+        }
+    }
+    if (pl.cluster) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (p.advance && group == 0 && tid == 0 && pos >= 0) c.pos[b] = pos + 1;
+    }
+}
+
+// Joins the splits of a window, one warp a head, and advances the positions.
+template <int DV>
+__global__ void __launch_bounds__(128) ska_q8_join_kernel(const SkaQ8DecodeParams p, const Q8Plan pl) {
+    const SkaQ8Cache& c = p.c;
+    const int bh = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (bh >= c.B * c.H) return;
+    const int b = bh / c.H, pos = c.pos[b];
+    if (pos < 0) return;
+    const float* m = pl.m + (size_t)bh * pl.splits;
+    const float* l = pl.l + (size_t)bh * pl.splits;
+    float mx = -INFINITY;
+    for (int k = 0; k < pl.splits; ++k) mx = fmaxf(mx, m[k]);
+    float sum = 0.0f, a[DV / 32] = {};
+    for (int k = 0; k < pl.splits; ++k) {
+        if (m[k] == -INFINITY) continue;
+        const float f = ex2_fast(m[k] - mx);
+        sum = fmaf(f, l[k], sum);
+#pragma unroll
+        for (int i = 0; i < DV / 32; ++i)
+            a[i] = fmaf(f, pl.o[((size_t)bh * pl.splits + k) * DV + 32 * i + lane], a[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < DV / 32; ++i)
+        static_cast<__nv_bfloat16*>(p.o)[(size_t)bh * DV + 32 * i + lane] = __float2bfloat16_rn(a[i] / sum);
+    // a sequence's other warps only ask whether pos is negative
+    if (p.advance && bh % c.H == 0 && lane == 0) c.pos[b] = pos + 1;
 }
 
 __global__ void ska_q8_advance_kernel(int* pos, int B) {
@@ -234,21 +525,90 @@ __global__ void ska_q8_advance_kernel(int* pos, int B) {
     if (b < B && pos[b] >= 0) pos[b] += 1;
 }
 
+// Heads of a group: as many as keep all eight warps busy (8, or fewer that leave
+// two, four or eight warps to each), the fewest groups among the best.
+int group_heads(int H) {
+    int best = 1;
+    double most = 0.0;
+    for (int groups = (H + 7) / 8; groups <= H && groups <= (H + 7) / 8 + 8; ++groups) {
+        const int G = (H + groups - 1) / groups;
+        if ((H + G - 1) / G != groups) continue;
+        const double used = (double)H * (kWarps / G) / ((double)groups * kWarps);
+        if (used > most + 1e-9) {
+            most = used;
+            best = G;
+        }
+    }
+    return best;
+}
+
+Q8Plan plan(const SkaQ8DecodeParams& p) {
+    Q8Plan pl;
+    pl.G = group_heads(p.c.H);
+    pl.groups = (p.c.H + pl.G - 1) / pl.G;
+    const long long units = (long long)p.c.B * pl.groups;
+    // two CTAs an SM; each split of at least 256 slots, in multiples of the largest block
+    long long P = units > 0 ? 2LL * sm_count() / units : 1;
+    const long long most = (p.c.window + 255) / 256;
+    if (P > most) P = most;
+    if (P < 1) P = 1;
+    const int range = (int)((p.c.window + P - 1) / P + 63) / 64 * 64;
+    pl.range = range;
+    pl.splits = (p.c.window + range - 1) / range;
+    pl.cluster = 0;
+    pl.m = pl.l = pl.o = nullptr;
+    return pl;
+}
+
+size_t plan_bytes(const SkaQ8DecodeParams& p, const Q8Plan& pl) {
+    return pl.splits == 1 ? 0 : (size_t)p.c.B * p.c.H * pl.splits * (p.c.dv + 2) * 4;
+}
+
 template <bool I8, int DK, int DV>
-cudaError_t launch_decode_cfg(const SkaQ8DecodeParams& p, cudaStream_t s) {
-    auto kern = ska_q8_decode_kernel<I8, DK, DV>;
-    const size_t smem = (size_t)p.c.window * 4;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+cudaError_t launch_decode_cfg(const SkaQ8DecodeParams& p, Q8Plan pl, cudaStream_t s) {
+    const size_t need = plan_bytes(p, pl);
+    if (need && p.ws_bytes < need) {
+        pl.splits = 1;
+        pl.range = (p.c.window + 63) / 64 * 64;
+    }
+    if (pl.splits > 1) {
+        const size_t rows = (size_t)p.c.B * p.c.H * pl.splits;
+        pl.o = static_cast<float*>(p.ws);
+        pl.m = pl.o + rows * DV;
+        pl.l = pl.m + rows;
+    }
+    pl.cluster = pl.splits == 1 && pl.groups <= 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)p.c.B * pl.groups), pl.splits);
+    cfg.blockDim = dim3(kDecThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    if (pl.cluster) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = pl.groups;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    cudaError_t e = cudaLaunchKernelEx(&cfg, ska_q8_decode_kernel<I8, DK, DV>, p, pl);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(p.c.B * p.c.H), kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    if (pl.splits > 1) {
+        ska_q8_join_kernel<DV><<<(unsigned)(((long long)p.c.B * p.c.H + 3) / 4), 128, 0, s>>>(p, pl);
+        e = cudaGetLastError();
+    } else if (!pl.cluster && p.advance) {
+        ska_q8_advance_kernel<<<(p.c.B + 255) / 256, 256, 0, s>>>(p.c.pos, p.c.B);
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 template <bool I8>
 cudaError_t launch_decode_t(const SkaQ8DecodeParams& p, cudaStream_t s) {
+    const Q8Plan pl = plan(p);
     if (p.c.dk == 64)
-        return p.c.dv == 64 ? launch_decode_cfg<I8, 64, 64>(p, s) : launch_decode_cfg<I8, 64, 128>(p, s);
-    return p.c.dv == 64 ? launch_decode_cfg<I8, 128, 64>(p, s) : launch_decode_cfg<I8, 128, 128>(p, s);
+        return p.c.dv == 64 ? launch_decode_cfg<I8, 64, 64>(p, pl, s) : launch_decode_cfg<I8, 64, 128>(p, pl, s);
+    return p.c.dv == 64 ? launch_decode_cfg<I8, 128, 64>(p, pl, s) : launch_decode_cfg<I8, 128, 128>(p, pl, s);
 }
 
 }  // namespace
@@ -261,13 +621,10 @@ cudaError_t launch_ska_q8_fill(const SkaQ8FillParams& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-size_t ska_q8_decode_workspace(const SkaQ8DecodeParams&) { return 0; }
+size_t ska_q8_decode_workspace(const SkaQ8DecodeParams& p) { return plan_bytes(p, plan(p)); }
 
 cudaError_t launch_ska_q8_decode(const SkaQ8DecodeParams& p, cudaStream_t s) {
-    const cudaError_t e = p.c.int8 ? launch_decode_t<true>(p, s) : launch_decode_t<false>(p, s);
-    if (e != cudaSuccess || !p.advance) return e;
-    ska_q8_advance_kernel<<<(p.c.B + 255) / 256, 256, 0, s>>>(p.c.pos, p.c.B);
-    return cudaGetLastError();
+    return p.c.int8 ? launch_decode_t<true>(p, s) : launch_decode_t<false>(p, s);
 }
 
 }  // namespace rdm

@@ -439,7 +439,7 @@ rdm_status rdm_ska_decode(const rdm_ska_decode_args *args, rdm_stream_t stream);
  *     codes -127 .. 127 by rounding value / scale to nearest even.
  *   A block of zeros has the scale 1.  Keys and values are meant to be finite:
  *   others do not count for the scale; infinities take the largest code, NaN
- *   stays NaN in e4m3 and becomes 0 in int8.  Decoding uses any scales it finds.
+ *   stays NaN in e4m3 and becomes 0 in int8.  Decoding takes any positive scales.
  */
 typedef enum { RDM_CACHE_E4M3 = 0, RDM_CACHE_INT8 = 1 } rdm_cache_type;
 
