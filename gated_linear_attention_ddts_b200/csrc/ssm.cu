@@ -101,27 +101,61 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
         if (p.dfeed) feed[e] = p.dfeed[hc];
     }
 
-    for (int t0 = begin; t0 < end; t0 += kTile) {
-        for (int unit = tid; unit < UNITS; unit += TH) {
-            const int q = unit / (CPB / 2), tq = t0 + 4 * q;
-            float2 xv[7];
+    // The next tile's inputs are on their way while this one's recurrence runs.
+    using Raw = typename Pair<T>::Raw;
+    using Quad = typename Four<T>::Raw;
+    constexpr int BC = (kTile * N / 4 + TH - 1) / TH;
+    static_assert(UNITS <= TH, "one unit a thread");
+    const bool has_unit = tid < UNITS;
+    const int uq = tid / (CPB / 2);
+    Raw xr[7], dr[4], zr[4], zc[4];
+    Quad br[BC], cr[BC];
+    auto fetch = [&](int t0) {
+        if (has_unit) {
+            const int tq = t0 + 4 * uq;
 #pragma unroll
             for (int i = 0; i < 7; ++i) {
                 const int t = tq - 3 + i;
-                xv[i] = make_float2(0.0f, 0.0f);
+                xr[i] = Pair<T>::zero();
                 if (i < 3 && p.W < 4 - i) continue;  // 3 - i tokens back: not in the filter
                 if (t >= 0) {
-                    if (t < end) xv[i] = Pair<T>::f(ldpair(x + (size_t)t * p.D + cp));
+                    if (t < end) xr[i] = ldpair(x + (size_t)t * p.D + cp);
                 } else if (cs && t >= 1 - p.W) {
-                    xv[i] = Pair<T>::f(ldpair(cs + (size_t)(p.W - 1 + t) * p.D + cp));
+                    xr[i] = ldpair(cs + (size_t)(p.W - 1 + t) * p.D + cp);
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool live = tq + j < end;
+                dr[j] = live ? ldpair(dt + (size_t)(tq + j) * p.D + cp) : Pair<T>::zero();
+                if (!LOCAL) zr[j] = z && live ? ldpair(z + (size_t)(tq + j) * p.D + cp) : Pair<T>::zero();
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < BC; ++k) {
+            const int i = tid + k * TH, t = t0 + i / (N / 4), n = 4 * (i % (N / 4));
+            br[k] = cr[k] = Four<T>::zero();
+            if (t < end) {
+                br[k] = Four<T>::ld(Bm + (size_t)t * N + n);
+                if (!LOCAL) cr[k] = Four<T>::ld(Cm + (size_t)t * N + n);
+            }
+        }
+    };
+    if (begin < end) fetch(begin);
+    const int place = L::place(ch);
+
+    for (int t0 = begin; t0 < end; t0 += kTile) {
+        if (has_unit) {
+            const int tq = t0 + 4 * uq;
+            float2 xv[7];
+#pragma unroll
+            for (int i = 0; i < 7; ++i) xv[i] = Pair<T>::f(xr[i]);
             float du[2][4], uu[2][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool live = tq + j < end;
-                float2 d = make_float2(0.0f, 0.0f);
-                if (live) d = Pair<T>::f(ldpair(dt + (size_t)(tq + j) * p.D + cp));
+                float2 d = Pair<T>::f(dr[j]);
+                zc[j] = zr[j];
                 float u0 = xv[3 + j].x, u1 = xv[3 + j].y;
                 if (p.W) {
                     float z0 = cb[0], z1 = cb[1];
@@ -146,23 +180,19 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                *reinterpret_cast<float4*>(sD[q][pl + e * L::ODD]) = make_float4(du[e][0], du[e][1], du[e][2], du[e][3]);
-                *reinterpret_cast<float4*>(sU[q][pl + e * L::ODD]) = make_float4(uu[e][0], uu[e][1], uu[e][2], uu[e][3]);
+                *reinterpret_cast<float4*>(sD[uq][pl + e * L::ODD]) = make_float4(du[e][0], du[e][1], du[e][2], du[e][3]);
+                *reinterpret_cast<float4*>(sU[uq][pl + e * L::ODD]) = make_float4(uu[e][0], uu[e][1], uu[e][2], uu[e][3]);
             }
         }
-        for (int i = tid; i < kTile * N / 4; i += TH) {
-            const int t = t0 + i / (N / 4), n = 4 * (i % (N / 4));
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = v;
-            if (t < end) {
-                v = ld4(Bm + (size_t)t * N + n);
-                if (!LOCAL) u = ld4(Cm + (size_t)t * N + n);
-            }
-            *reinterpret_cast<float4*>(&sB[t - t0][n]) = v;
-            if (!LOCAL) *reinterpret_cast<float4*>(&sC[t - t0][n]) = u;
+#pragma unroll
+        for (int k = 0; k < BC; ++k) {
+            const int i = tid + k * TH;
+            *reinterpret_cast<float4*>(&sB[0][0] + 4 * i) = Four<T>::f(br[k]);
+            if (!LOCAL) *reinterpret_cast<float4*>(&sC[0][0] + 4 * i) = Four<T>::f(cr[k]);
         }
         __syncthreads();
-        const int place = L::place(ch);
-#pragma unroll 1
+        if (t0 + kTile < end) fetch(t0 + kTile);
+#pragma unroll 4
         for (int q = 0; q < kTile / 4; ++q) {
             if (!LOCAL && p.saved && (q & 3) == 0 && t0 + 4 * q < end) {
                 const size_t nc = (p.T + kSsmChunk - 1) / kSsmChunk;
@@ -194,31 +224,29 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
             }
         }
         __syncthreads();
-        if (!LOCAL && p.y) {
-            for (int unit = tid; unit < UNITS; unit += TH) {
-                const int q = unit / (CPB / 2), tq = t0 + 4 * q;
-                float yv[2][4];
+        if (!LOCAL && p.y && has_unit) {
+            const int tq = t0 + 4 * uq;
+            float yv[2][4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float4 a = *reinterpret_cast<const float4*>(sY[q][pl + e * L::ODD]);
-                    const float4 u = *reinterpret_cast<const float4*>(sU[q][pl + e * L::ODD]);
-                    yv[e][0] = fmaf(feed[e], u.x, a.x); yv[e][1] = fmaf(feed[e], u.y, a.y);
-                    yv[e][2] = fmaf(feed[e], u.z, a.z); yv[e][3] = fmaf(feed[e], u.w, a.w);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (tq + j >= end) continue;
-                    float2 g = make_float2(1.0f, 1.0f);
-                    if (z) {
-                        g = Pair<T>::f(ldpair(z + (size_t)(tq + j) * p.D + cp));
-                        g.x = silu(g.x);
-                        g.y = silu(g.y);
-                    }
-                    stpair(y + (size_t)(tq + j) * p.D + cp, yv[0][j] * g.x, yv[1][j] * g.y);
-                }
+            for (int e = 0; e < 2; ++e) {
+                const float4 a = *reinterpret_cast<const float4*>(sY[uq][pl + e * L::ODD]);
+                const float4 u = *reinterpret_cast<const float4*>(sU[uq][pl + e * L::ODD]);
+                yv[e][0] = fmaf(feed[e], u.x, a.x); yv[e][1] = fmaf(feed[e], u.y, a.y);
+                yv[e][2] = fmaf(feed[e], u.z, a.z); yv[e][3] = fmaf(feed[e], u.w, a.w);
             }
-            // sU is written again by the threads that read it here; sY only behind the next barrier
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (tq + j >= end) continue;
+                float2 g = make_float2(1.0f, 1.0f);
+                if (z) {
+                    g = Pair<T>::f(zc[j]);
+                    g.x = silu(g.x);
+                    g.y = silu(g.y);
+                }
+                stpair(y + (size_t)(tq + j) * p.D + cp, yv[0][j] * g.x, yv[1][j] * g.y);
+            }
         }
+        // sU is written again by the threads that read it here; sY only behind the next barrier
     }
     if (LOCAL) {
         const size_t states = (size_t)p.B * p.H * p.D;

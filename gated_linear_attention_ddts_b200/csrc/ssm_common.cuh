@@ -61,13 +61,28 @@ template <typename T>
 __device__ __forceinline__ void stpair(T* p, float a, float b) {
     *reinterpret_cast<typename Pair<T>::Raw*>(p) = Pair<T>::r(a, b);
 }
-// four neighbouring values as float32
-__device__ __forceinline__ float4 ld4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
+// Four neighbouring values as loaded, and as float32.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+    using Raw = float4;
+    static __device__ __forceinline__ Raw zero() { return make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    static __device__ __forceinline__ Raw ld(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+    static __device__ __forceinline__ float4 f(Raw r) { return r; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+    using Raw = uint2;
+    static __device__ __forceinline__ Raw zero() { return make_uint2(0u, 0u); }
+    static __device__ __forceinline__ Raw ld(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
+    static __device__ __forceinline__ float4 f(Raw r) {
+        return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
+                           __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+    }
+};
+template <typename T>
+__device__ __forceinline__ float4 ld4(const T* p) { return Four<T>::f(Four<T>::ld(p)); }
 
 // Sums of four values over the LPC lanes of a channel (LPC >= 4 neighbouring
 // lanes): lane l ends with the sum of value l & 3.  Three shuffles for the first
