@@ -21,6 +21,8 @@
 // first launch runs every segment but the last from a zero state and leaves its
 // end state and its sum of delta; in the second each block folds the segments
 // before its own, s <- local + exp(A sum delta) s, and runs for good.
+#include <type_traits>
+
 #include "launch.h"
 #include "ssm_common.cuh"
 
@@ -45,8 +47,12 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
     __shared__ __align__(16) float sD[kTile / 4][L::PLACES][4];
     __shared__ __align__(16) float sU[kTile / 4][L::PLACES][4];
     __shared__ __align__(16) float sY[kTile / 4][L::PLACES][4];
-    __shared__ __align__(16) float sB[kTile][N];
-    __shared__ __align__(16) float sC[LOCAL ? 1 : kTile][N];
+    // B and C in their own type: four bf16 states are one 8-byte read a lane, half of
+    // the shared-memory wavefronts of float32 (they bound the loop before the
+    // exponentials did)
+    using Quad = typename Four<T>::Raw;
+    __shared__ __align__(16) Quad sB[kTile][N / 4];
+    __shared__ __align__(16) Quad sC[LOCAL ? 1 : kTile][N / 4];
     const int nblk = p.D / CPB;
     const int bh = blockIdx.x / nblk, c0 = (blockIdx.x % nblk) * CPB;
     const int b = bh / p.H, h = bh % p.H, seg = blockIdx.y;
@@ -69,24 +75,25 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
     // the recurrence's part of this thread: states 4 sl .. 4 sl + 3 of channel ch
     const int ch = tid / LPC, sl = tid % LPC;
     const size_t srow = ((size_t)bh * p.D + c0 + ch) * N + 4 * sl;
-    float A2[4], s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dsum = 0.0f;
+    float2 A2[2], s[2] = {two(0.0f), two(0.0f)};
+    float dsum = 0.0f;
     {
         const float4 a = ld4(p.A + ((size_t)h * p.D + c0 + ch) * N + 4 * sl);
-        A2[0] = a.x * kLog2e; A2[1] = a.y * kLog2e; A2[2] = a.z * kLog2e; A2[3] = a.w * kLog2e;
+        A2[0] = make_float2(a.x * kLog2e, a.y * kLog2e);
+        A2[1] = make_float2(a.z * kLog2e, a.w * kLog2e);
     }
     if (!LOCAL) {
         if (p.S0) {
             const float4 v = ld4(p.S0 + srow);
-            s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
+            s[0] = make_float2(v.x, v.y);
+            s[1] = make_float2(v.z, v.w);
         }
         const size_t states = (size_t)p.B * p.H * p.D;
         for (int j = 0; j < seg; ++j) {  // the segments before this one
             const float4 v = *reinterpret_cast<const float4*>(sg.local + j * states * N + srow);
-            const float ds = sg.dsum[j * states + (size_t)bh * p.D + c0 + ch];
-            s[0] = fmaf(ex2_fast(A2[0] * ds), s[0], v.x);
-            s[1] = fmaf(ex2_fast(A2[1] * ds), s[1], v.y);
-            s[2] = fmaf(ex2_fast(A2[2] * ds), s[2], v.z);
-            s[3] = fmaf(ex2_fast(A2[3] * ds), s[3], v.w);
+            const float2 ds = two(sg.dsum[j * states + (size_t)bh * p.D + c0 + ch]);
+            s[0] = fma2(ex22(mul2(A2[0], ds)), s[0], make_float2(v.x, v.y));
+            s[1] = fma2(ex22(mul2(A2[1], ds)), s[1], make_float2(v.z, v.w));
         }
     }
     // the element-wise part: channels cp, cp + 1 of tokens 4 uq .. 4 uq + 3
@@ -95,7 +102,9 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int hc = h * p.D + c0 + cp + e;
-        for (int i = 0; i < p.W; ++i) w[i][e] = p.cw[(size_t)hc * p.W + i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < p.W) w[i][e] = p.cw[(size_t)hc * p.W + i];
         if (p.cb) cb[e] = p.cb[hc];
         if (p.dt_bias) bias[e] = p.dt_bias[hc];
         if (p.dfeed) feed[e] = p.dfeed[hc];
@@ -103,14 +112,18 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
 
     // The next tile's inputs are on their way while this one's recurrence runs.
     using Raw = typename Pair<T>::Raw;
-    using Quad = typename Four<T>::Raw;
-    constexpr int BC = (kTile * N / 4 + TH - 1) / TH;
-    static_assert(UNITS <= TH, "one unit a thread");
+    constexpr int BC = kTile * N / 4 / TH;
+    static_assert(UNITS <= TH && BC * TH * 4 == kTile * N, "one unit a thread, whole rounds of B and C");
     const bool has_unit = tid < UNITS;
     const int uq = tid / (CPB / 2);
+    const unsigned off = (unsigned)(4 * uq) * p.D + cp;
     Raw xr[7], dr[4], zr[4], zc[4];
     Quad br[BC], cr[BC];
-    auto fetch = [&](int t0) {
+    // A tile whose tokens are all there and not the sequence's first needs no tests.
+    auto whole = [&](int t0) { return t0 >= 4 && t0 + kTile <= end; };
+    auto fetch = [&](int t0, auto inner) {
+        constexpr bool IN = decltype(inner)::value;
+        const T *xt = x + (size_t)t0 * p.D, *dtt = dt + (size_t)t0 * p.D, *zt = z + (size_t)t0 * p.D;
         if (has_unit) {
             const int tq = t0 + 4 * uq;
 #pragma unroll
@@ -118,7 +131,9 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
                 const int t = tq - 3 + i;
                 xr[i] = Pair<T>::zero();
                 if (i < 3 && p.W < 4 - i) continue;  // 3 - i tokens back: not in the filter
-                if (t >= 0) {
+                if (IN) {
+                    xr[i] = ldpair(xt + (i - 3) * p.D + off);
+                } else if (t >= 0) {
                     if (t < end) xr[i] = ldpair(x + (size_t)t * p.D + cp);
                 } else if (cs && t >= 1 - p.W) {
                     xr[i] = ldpair(cs + (size_t)(p.W - 1 + t) * p.D + cp);
@@ -126,25 +141,23 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool live = tq + j < end;
-                dr[j] = live ? ldpair(dt + (size_t)(tq + j) * p.D + cp) : Pair<T>::zero();
-                if (!LOCAL) zr[j] = z && live ? ldpair(z + (size_t)(tq + j) * p.D + cp) : Pair<T>::zero();
+                const bool live = IN || tq + j < end;
+                dr[j] = live ? ldpair(dtt + j * p.D + off) : Pair<T>::zero();
+                if (!LOCAL) zr[j] = z && live ? ldpair(zt + j * p.D + off) : Pair<T>::zero();
             }
         }
 #pragma unroll
         for (int k = 0; k < BC; ++k) {
-            const int i = tid + k * TH, t = t0 + i / (N / 4), n = 4 * (i % (N / 4));
+            const int i = tid + k * TH, t = t0 + i / (N / 4);
             br[k] = cr[k] = Four<T>::zero();
-            if (t < end) {
-                br[k] = Four<T>::ld(Bm + (size_t)t * N + n);
-                if (!LOCAL) cr[k] = Four<T>::ld(Cm + (size_t)t * N + n);
+            if (IN || t < end) {
+                br[k] = Four<T>::ld(Bm + (size_t)t0 * N + 4 * i);
+                if (!LOCAL) cr[k] = Four<T>::ld(Cm + (size_t)t0 * N + 4 * i);
             }
         }
     };
-    if (begin < end) fetch(begin);
-    const int place = L::place(ch);
-
-    for (int t0 = begin; t0 < end; t0 += kTile) {
+    auto stage = [&](int t0, auto inner) {
+        constexpr bool IN = decltype(inner)::value;
         if (has_unit) {
             const int tq = t0 + 4 * uq;
             float2 xv[7];
@@ -153,7 +166,7 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
             float du[2][4], uu[2][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool live = tq + j < end;
+                const bool live = IN || tq + j < end;
                 float2 d = Pair<T>::f(dr[j]);
                 zc[j] = zr[j];
                 float u0 = xv[3 + j].x, u1 = xv[3 + j].y;
@@ -186,18 +199,51 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
         }
 #pragma unroll
         for (int k = 0; k < BC; ++k) {
-            const int i = tid + k * TH;
-            *reinterpret_cast<float4*>(&sB[0][0] + 4 * i) = Four<T>::f(br[k]);
-            if (!LOCAL) *reinterpret_cast<float4*>(&sC[0][0] + 4 * i) = Four<T>::f(cr[k]);
+            (&sB[0][0])[tid + k * TH] = br[k];
+            if (!LOCAL) (&sC[0][0])[tid + k * TH] = cr[k];
         }
+    };
+    auto finish = [&](int t0, auto inner) {  // y of the unit, with the skip and the gate
+        constexpr bool IN = decltype(inner)::value;
+        const int tq = t0 + 4 * uq;
+        T* yt = y + (size_t)t0 * p.D;
+        float yv[2][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float4 a = *reinterpret_cast<const float4*>(sY[uq][pl + e * L::ODD]);
+            const float4 u = *reinterpret_cast<const float4*>(sU[uq][pl + e * L::ODD]);
+            yv[e][0] = fmaf(feed[e], u.x, a.x); yv[e][1] = fmaf(feed[e], u.y, a.y);
+            yv[e][2] = fmaf(feed[e], u.z, a.z); yv[e][3] = fmaf(feed[e], u.w, a.w);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!IN && tq + j >= end) continue;
+            if (z) {
+                const float2 g = Pair<T>::f(zc[j]);
+                yv[0][j] *= silu(g.x);
+                yv[1][j] *= silu(g.y);
+            }
+            stpair(yt + j * p.D + off, yv[0][j], yv[1][j]);
+        }
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (begin < end) fetch(begin, No());
+    const int place = L::place(ch);
+
+    for (int t0 = begin; t0 < end; t0 += kTile) {
+        const bool in = whole(t0);
+        if (in) stage(t0, Yes());
+        else stage(t0, No());
         __syncthreads();
-        if (t0 + kTile < end) fetch(t0 + kTile);
+        if (whole(t0 + kTile)) fetch(t0 + kTile, Yes());
+        else if (t0 + kTile < end) fetch(t0 + kTile, No());
 #pragma unroll 4
         for (int q = 0; q < kTile / 4; ++q) {
             if (!LOCAL && p.saved && (q & 3) == 0 && t0 + 4 * q < end) {
                 const size_t nc = (p.T + kSsmChunk - 1) / kSsmChunk;
                 const size_t at = (((size_t)bh * nc + (t0 + 4 * q) / kSsmChunk) * p.D + c0 + ch) * N + 4 * sl;
-                *reinterpret_cast<float4*>(p.saved + at) = make_float4(s[0], s[1], s[2], s[3]);
+                *reinterpret_cast<float4*>(p.saved + at) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
             }
             const float4 d4 = *reinterpret_cast<const float4*>(sD[q][place]);
             const float4 u4 = *reinterpret_cast<const float4*>(sU[q][place]);
@@ -205,17 +251,16 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
             float yy[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float4 bb = *reinterpret_cast<const float4*>(&sB[4 * q + j][4 * sl]);
-                const float du = dd[j] * uu[j];
-                s[0] = fmaf(ex2_fast(dd[j] * A2[0]), s[0], du * bb.x);
-                s[1] = fmaf(ex2_fast(dd[j] * A2[1]), s[1], du * bb.y);
-                s[2] = fmaf(ex2_fast(dd[j] * A2[2]), s[2], du * bb.z);
-                s[3] = fmaf(ex2_fast(dd[j] * A2[3]), s[3], du * bb.w);
+                const Quad bq = sB[4 * q + j][sl];
+                const float2 d2 = two(dd[j]), du = two(dd[j] * uu[j]);
+                s[0] = fma2(ex22(mul2(d2, A2[0])), s[0], mul2(du, Four<T>::lo(bq)));
+                s[1] = fma2(ex22(mul2(d2, A2[1])), s[1], mul2(du, Four<T>::hi(bq)));
                 if (LOCAL) {
                     dsum += dd[j];
                 } else {
-                    const float4 cc = *reinterpret_cast<const float4*>(&sC[4 * q + j][4 * sl]);
-                    yy[j] = fmaf(s[0], cc.x, fmaf(s[1], cc.y, fmaf(s[2], cc.z, s[3] * cc.w)));
+                    const Quad cq = sC[4 * q + j][sl];
+                    const float2 v = fma2(s[1], Four<T>::hi(cq), mul2(s[0], Four<T>::lo(cq)));
+                    yy[j] = v.x + v.y;
                 }
             }
             if (!LOCAL) {
@@ -225,37 +270,19 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
         }
         __syncthreads();
         if (!LOCAL && p.y && has_unit) {
-            const int tq = t0 + 4 * uq;
-            float yv[2][4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float4 a = *reinterpret_cast<const float4*>(sY[uq][pl + e * L::ODD]);
-                const float4 u = *reinterpret_cast<const float4*>(sU[uq][pl + e * L::ODD]);
-                yv[e][0] = fmaf(feed[e], u.x, a.x); yv[e][1] = fmaf(feed[e], u.y, a.y);
-                yv[e][2] = fmaf(feed[e], u.z, a.z); yv[e][3] = fmaf(feed[e], u.w, a.w);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (tq + j >= end) continue;
-                float2 g = make_float2(1.0f, 1.0f);
-                if (z) {
-                    g = Pair<T>::f(zc[j]);
-                    g.x = silu(g.x);
-                    g.y = silu(g.y);
-                }
-                stpair(y + (size_t)(tq + j) * p.D + cp, yv[0][j] * g.x, yv[1][j] * g.y);
-            }
+            if (in) finish(t0, Yes());
+            else finish(t0, No());
         }
         // sU is written again by the threads that read it here; sY only behind the next barrier
     }
     if (LOCAL) {
         const size_t states = (size_t)p.B * p.H * p.D;
-        *reinterpret_cast<float4*>(sg.local + seg * states * N + srow) = make_float4(s[0], s[1], s[2], s[3]);
+        *reinterpret_cast<float4*>(sg.local + seg * states * N + srow) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
         if (sl == 0) sg.dsum[seg * states + (size_t)bh * p.D + c0 + ch] = dsum;
         return;
     }
     if (!last) return;
-    if (p.ST) *reinterpret_cast<float4*>(p.ST + srow) = make_float4(s[0], s[1], s[2], s[3]);
+    if (p.ST) *reinterpret_cast<float4*>(p.ST + srow) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
     if (p.cs_out) {  // the last W-1 inputs, some of them perhaps carried in
         T* out = static_cast<T*>(p.cs_out) + (size_t)bh * (p.W - 1) * p.D + c0;
         for (int i = tid; i < (p.W - 1) * CPB; i += TH) {

@@ -13,23 +13,44 @@ namespace ssm {
 // would leave only 12 of their bits; so log1p(y) = 2 atanh(s), s = y / (2 + y),
 // as 2 s P(s^2) with s^2 <= 1/9 (P fitted here, relative error 4e-9), which the
 // float32 states and gradients need.
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float softplus(float x) {
     const float y = ex2_fast(-fabsf(x) * kLog2e);
-    const float s = __fdividef(y, 2.0f + y);
+    const float s = y * rcp_fast(2.0f + y);
     const float q = s * s;
     float r = 0.2817833423614502f;
     r = fmaf(r, q, 0.27960604429244995f);
     r = fmaf(r, q, 0.40024909377098083f);
     r = fmaf(r, q, 0.6666631698608398f);
     r = fmaf(r, q, 2.0f);
-    return x != x ? x : fmaf(s, r, fmaxf(x, 0.0f));
+    return fmaf(s, r, fmaxf(x, 0.0f));  // NaN comes through s
 }
-__device__ __forceinline__ float sigmoid(float x) {
-    return __fdividef(1.0f, 1.0f + ex2_fast(fminf(-x * kLog2e, 126.0f)));
-}
+__device__ __forceinline__ float sigmoid(float x) { return rcp_fast(1.0f + ex2_fast(-x * kLog2e)); }
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 // d silu(x) / dx = s (1 + x (1 - s))
 __device__ __forceinline__ float dsilu(float x, float s) { return s * fmaf(x, 1.0f - s, 1.0f); }
+
+// Two float32 operations an instruction (sm_100's packed forms), each rounded as
+// the single one.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 ex22(float2 x) { return make_float2(ex2_fast(x.x), ex2_fast(x.y)); }
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
 
 // Two neighbouring channels of a row.
 template <typename T>
@@ -69,20 +90,27 @@ struct Four<float> {
     using Raw = float4;
     static __device__ __forceinline__ Raw zero() { return make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
     static __device__ __forceinline__ Raw ld(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-    static __device__ __forceinline__ float4 f(Raw r) { return r; }
+    static __device__ __forceinline__ float2 lo(Raw r) { return make_float2(r.x, r.y); }
+    static __device__ __forceinline__ float2 hi(Raw r) { return make_float2(r.z, r.w); }
 };
 template <>
 struct Four<__nv_bfloat16> {
     using Raw = uint2;
     static __device__ __forceinline__ Raw zero() { return make_uint2(0u, 0u); }
     static __device__ __forceinline__ Raw ld(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
-    static __device__ __forceinline__ float4 f(Raw r) {
-        return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
-                           __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+    static __device__ __forceinline__ float2 lo(Raw r) {
+        return make_float2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
+    }
+    static __device__ __forceinline__ float2 hi(Raw r) {
+        return make_float2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
     }
 };
 template <typename T>
-__device__ __forceinline__ float4 ld4(const T* p) { return Four<T>::f(Four<T>::ld(p)); }
+__device__ __forceinline__ float4 ld4(const T* p) {
+    const typename Four<T>::Raw r = Four<T>::ld(p);
+    const float2 a = Four<T>::lo(r), b = Four<T>::hi(r);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
 
 // Sums of four values over the LPC lanes of a channel (LPC >= 4 neighbouring
 // lanes): lane l ends with the sum of value l & 3.  Three shuffles for the first
