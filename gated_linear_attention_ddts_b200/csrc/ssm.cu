@@ -40,19 +40,49 @@ struct SegArgs {
     float *local, *dsum;
 };
 
+// 16 bytes from global into shared memory without passing registers; zeros where
+// `there` is false.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+// Threads of the element-wise warps: one for each two channels by four tokens of
+// a tile.
+template <int CPB>
+constexpr int kEw = (kTile / 4) * (CPB / 2) < 32 ? 32 : (kTile / 4) * (CPB / 2);
+
+// B and C are staged in their own type: four bf16 states are one 8-byte read a
+// lane, half of the shared-memory wavefronts of float32 (which bounded the loop
+// before the exponentials did).
 template <typename T, int N, int CPB, bool LOCAL>
-__global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p, const SegArgs sg) {
+struct FwdSmem {
+    float D[2][kTile / 4][Lay<N, CPB>::PLACES][4];
+    float U[2][kTile / 4][Lay<N, CPB>::PLACES][4];
+    float Y[LOCAL ? 1 : 2][LOCAL ? 1 : kTile / 4][Lay<N, CPB>::PLACES][4];
+    typename Four<T>::Raw B[3][kTile][N / 4];
+    typename Four<T>::Raw C[LOCAL ? 1 : 3][LOCAL ? 1 : kTile][N / 4];
+};
+
+// Two kinds of warps, a tile apart, one block barrier a tile: while the scan warps
+// run the recurrence over tile k, the element-wise warps finish y of tile k - 1
+// and make delta and u of tile k + 1, whose inputs they fetched a tile ago.  With
+// one kind doing all three in turn only 58% of the issue slots were used (2.6
+// warps a scheduler at B8 H24 D64, each waiting for itself): 190 us against 165.
+template <typename T, int N, int CPB, bool LOCAL>
+__global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 2 : 3)
+    ssm_fwd_kernel(const SsmParams p, const SegArgs sg) {
     using L = Lay<N, CPB>;
-    constexpr int LPC = L::LPC, TH = L::THREADS, UNITS = (kTile / 4) * (CPB / 2);
-    __shared__ __align__(16) float sD[kTile / 4][L::PLACES][4];
-    __shared__ __align__(16) float sU[kTile / 4][L::PLACES][4];
-    __shared__ __align__(16) float sY[kTile / 4][L::PLACES][4];
-    // B and C in their own type: four bf16 states are one 8-byte read a lane, half of
-    // the shared-memory wavefronts of float32 (they bound the loop before the
-    // exponentials did)
+    constexpr int LPC = L::LPC, TH = L::THREADS, EW = kEw<CPB>, UNITS = (kTile / 4) * (CPB / 2);
     using Quad = typename Four<T>::Raw;
-    __shared__ __align__(16) Quad sB[kTile][N / 4];
-    __shared__ __align__(16) Quad sC[LOCAL ? 1 : kTile][N / 4];
+    using Raw = typename Pair<T>::Raw;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    FwdSmem<T, N, CPB, LOCAL>& sm = *reinterpret_cast<FwdSmem<T, N, CPB, LOCAL>*>(smem_raw);
+    auto &sD = sm.D, &sU = sm.U;
+    auto& sY = sm.Y;
+    auto& sB = sm.B;
+    auto& sC = sm.C;
     const int nblk = p.D / CPB;
     const int bh = blockIdx.x / nblk, c0 = (blockIdx.x % nblk) * CPB;
     const int b = bh / p.H, h = bh % p.H, seg = blockIdx.y;
@@ -60,71 +90,40 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
     const int begin = seg * sg.len;
     if (LOCAL ? begin + sg.len >= len : (seg > 0 && begin >= len)) return;  // nothing after or in it
     const int end = LOCAL ? begin + sg.len : min(begin + sg.len, len);
-    const bool last = end == len;
-    const int tid = threadIdx.x;
+    const int tiles = (end - begin + kTile - 1) / kTile;
     const size_t row0 = (size_t)bh * p.T;
     const T* x = static_cast<const T*>(p.x) + row0 * p.D + c0;
-    const T* dt = static_cast<const T*>(p.dt) + row0 * p.D + c0;
-    const T* z = p.z ? static_cast<const T*>(p.z) + row0 * p.D + c0 : nullptr;
-    T* y = static_cast<T*>(p.y) + row0 * p.D + c0;
-    const size_t grow = (size_t)(b * p.G + h / (p.H / p.G)) * p.T;
-    const T* Bm = static_cast<const T*>(p.Bm) + grow * N;
-    const T* Cm = static_cast<const T*>(p.Cm) + grow * N;
     const T* cs = p.cs_in ? static_cast<const T*>(p.cs_in) + (size_t)bh * (p.W - 1) * p.D + c0 : nullptr;
 
-    // the recurrence's part of this thread: states 4 sl .. 4 sl + 3 of channel ch
-    const int ch = tid / LPC, sl = tid % LPC;
-    const size_t srow = ((size_t)bh * p.D + c0 + ch) * N + 4 * sl;
-    float2 A2[2], s[2] = {two(0.0f), two(0.0f)};
-    float dsum = 0.0f;
-    {
-        const float4 a = ld4(p.A + ((size_t)h * p.D + c0 + ch) * N + 4 * sl);
-        A2[0] = make_float2(a.x * kLog2e, a.y * kLog2e);
-        A2[1] = make_float2(a.z * kLog2e, a.w * kLog2e);
-    }
-    if (!LOCAL) {
-        if (p.S0) {
-            const float4 v = ld4(p.S0 + srow);
-            s[0] = make_float2(v.x, v.y);
-            s[1] = make_float2(v.z, v.w);
-        }
-        const size_t states = (size_t)p.B * p.H * p.D;
-        for (int j = 0; j < seg; ++j) {  // the segments before this one
-            const float4 v = *reinterpret_cast<const float4*>(sg.local + j * states * N + srow);
-            const float2 ds = two(sg.dsum[j * states + (size_t)bh * p.D + c0 + ch]);
-            s[0] = fma2(ex22(mul2(A2[0], ds)), s[0], make_float2(v.x, v.y));
-            s[1] = fma2(ex22(mul2(A2[1], ds)), s[1], make_float2(v.z, v.w));
-        }
-    }
-    // the element-wise part: channels cp, cp + 1 of tokens 4 uq .. 4 uq + 3
-    const int cp = 2 * (tid % (CPB / 2)), pl = cp >> 1;
-    float w[4][2] = {}, cb[2] = {0.0f, 0.0f}, bias[2] = {0.0f, 0.0f}, feed[2] = {0.0f, 0.0f};
+    if (threadIdx.x >= TH) {  // ---------------- element-wise warps
+        const int tid = threadIdx.x - TH;
+        const T* dt = static_cast<const T*>(p.dt) + row0 * p.D + c0;
+        const T* z = p.z ? static_cast<const T*>(p.z) + row0 * p.D + c0 : nullptr;
+        T* y = static_cast<T*>(p.y) + row0 * p.D + c0;
+        const size_t grow = (size_t)(b * p.G + h / (p.H / p.G)) * p.T;
+        const T* Bm = static_cast<const T*>(p.Bm) + grow * N;
+        const T* Cm = static_cast<const T*>(p.Cm) + grow * N;
+        // channels cp, cp + 1 of tokens 4 uq .. 4 uq + 3 of a tile
+        const bool has_unit = tid < UNITS;
+        const int uq = tid / (CPB / 2), cp = 2 * (tid % (CPB / 2)), pl = cp >> 1;
+        const unsigned off = (unsigned)(4 * uq) * p.D + cp;
+        float w[4][2] = {}, cb[2] = {0.0f, 0.0f}, bias[2] = {0.0f, 0.0f}, feed[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int hc = h * p.D + c0 + cp + e;
+        for (int e = 0; e < 2; ++e) {
+            const int hc = h * p.D + c0 + cp + e;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < p.W) w[i][e] = p.cw[(size_t)hc * p.W + i];
-        if (p.cb) cb[e] = p.cb[hc];
-        if (p.dt_bias) bias[e] = p.dt_bias[hc];
-        if (p.dfeed) feed[e] = p.dfeed[hc];
-    }
-
-    // The next tile's inputs are on their way while this one's recurrence runs.
-    using Raw = typename Pair<T>::Raw;
-    constexpr int BC = kTile * N / 4 / TH;
-    static_assert(UNITS <= TH && BC * TH * 4 == kTile * N, "one unit a thread, whole rounds of B and C");
-    const bool has_unit = tid < UNITS;
-    const int uq = tid / (CPB / 2);
-    const unsigned off = (unsigned)(4 * uq) * p.D + cp;
-    Raw xr[7], dr[4], zr[4], zc[4];
-    Quad br[BC], cr[BC];
-    // A tile whose tokens are all there and not the sequence's first needs no tests.
-    auto whole = [&](int t0) { return t0 >= 4 && t0 + kTile <= end; };
-    auto fetch = [&](int t0, auto inner) {
-        constexpr bool IN = decltype(inner)::value;
-        const T *xt = x + (size_t)t0 * p.D, *dtt = dt + (size_t)t0 * p.D, *zt = z + (size_t)t0 * p.D;
-        if (has_unit) {
+            for (int i = 0; i < 4; ++i)
+                if (i < p.W) w[i][e] = p.cw[(size_t)hc * p.W + i];
+            if (p.cb) cb[e] = p.cb[hc];
+            if (p.dt_bias) bias[e] = p.dt_bias[hc];
+            if (p.dfeed) feed[e] = p.dfeed[hc];
+        }
+        Raw xr[7], dr[4], zr[4];
+        // A tile whose tokens are all there and not the sequence's first needs no tests.
+        auto whole = [&](int t0) { return t0 >= 4 && t0 + kTile <= end; };
+        auto fetch = [&](int t0, auto inner) {
+            constexpr bool IN = decltype(inner)::value;
+            const T *xt = x + (size_t)t0 * p.D, *dtt = dt + (size_t)t0 * p.D;
             const int tq = t0 + 4 * uq;
 #pragma unroll
             for (int i = 0; i < 7; ++i) {
@@ -140,26 +139,27 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool live = IN || tq + j < end;
-                dr[j] = live ? ldpair(dtt + j * p.D + off) : Pair<T>::zero();
-                if (!LOCAL) zr[j] = z && live ? ldpair(zt + j * p.D + off) : Pair<T>::zero();
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < BC; ++k) {
-            const int i = tid + k * TH, t = t0 + i / (N / 4);
-            br[k] = cr[k] = Four<T>::zero();
-            if (IN || t < end) {
-                br[k] = Four<T>::ld(Bm + (size_t)t0 * N + 4 * i);
-                if (!LOCAL) cr[k] = Four<T>::ld(Cm + (size_t)t0 * N + 4 * i);
-            }
-        }
-    };
-    auto stage = [&](int t0, auto inner) {
-        constexpr bool IN = decltype(inner)::value;
-        if (has_unit) {
+            for (int j = 0; j < 4; ++j) dr[j] = IN || tq + j < end ? ldpair(dtt + j * p.D + off) : Pair<T>::zero();
+        };
+        auto fetch_z = [&](int t0) {
+            const T* zt = z + (size_t)t0 * p.D;
             const int tq = t0 + 4 * uq;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) zr[j] = tq + j < end ? ldpair(zt + j * p.D + off) : Pair<T>::zero();
+        };
+        auto copy_bc = [&](int tile) {
+            constexpr int PER = 16 / (int)sizeof(T), ROW = N / PER;  // values in 16 bytes, pieces of a token
+            const int t0 = begin + tile * kTile;
+            for (int i = tid; i < kTile * ROW; i += EW) {
+                const bool there = t0 + i / ROW < end;
+                const size_t at = (size_t)(there ? t0 : 0) * N + (there ? i * PER : 0);
+                copy16(reinterpret_cast<char*>(&sB[tile % 3][0][0]) + 16 * i, Bm + at, there);
+                if (!LOCAL) copy16(reinterpret_cast<char*>(&sC[tile % 3][0][0]) + 16 * i, Cm + at, there);
+            }
+        };
+        auto stage = [&](int tile, auto inner) {
+            constexpr bool IN = decltype(inner)::value;
+            const int tq = begin + tile * kTile + 4 * uq;
             float2 xv[7];
 #pragma unroll
             for (int i = 0; i < 7; ++i) xv[i] = Pair<T>::f(xr[i]);
@@ -168,7 +168,6 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
             for (int j = 0; j < 4; ++j) {
                 const bool live = IN || tq + j < end;
                 float2 d = Pair<T>::f(dr[j]);
-                zc[j] = zr[j];
                 float u0 = xv[3 + j].x, u1 = xv[3 + j].y;
                 if (p.W) {
                     float z0 = cb[0], z1 = cb[1];
@@ -193,99 +192,143 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_fwd_kernel(const SsmParams p,
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                *reinterpret_cast<float4*>(sD[uq][pl + e * L::ODD]) = make_float4(du[e][0], du[e][1], du[e][2], du[e][3]);
-                *reinterpret_cast<float4*>(sU[uq][pl + e * L::ODD]) = make_float4(uu[e][0], uu[e][1], uu[e][2], uu[e][3]);
+                const int at = pl + e * L::ODD;
+                *reinterpret_cast<float4*>(sD[tile & 1][uq][at]) = make_float4(du[e][0], du[e][1], du[e][2], du[e][3]);
+                *reinterpret_cast<float4*>(sU[tile & 1][uq][at]) = make_float4(uu[e][0], uu[e][1], uu[e][2], uu[e][3]);
             }
-        }
+        };
+        auto finish = [&](int tile, auto inner) {  // y of the unit, with the skip and the gate
+            constexpr bool IN = decltype(inner)::value;
+            const int t0 = begin + tile * kTile, tq = t0 + 4 * uq;
+            T* yt = y + (size_t)t0 * p.D;
+            float yv[2][4];
 #pragma unroll
-        for (int k = 0; k < BC; ++k) {
-            (&sB[0][0])[tid + k * TH] = br[k];
-            if (!LOCAL) (&sC[0][0])[tid + k * TH] = cr[k];
-        }
-    };
-    auto finish = [&](int t0, auto inner) {  // y of the unit, with the skip and the gate
-        constexpr bool IN = decltype(inner)::value;
-        const int tq = t0 + 4 * uq;
-        T* yt = y + (size_t)t0 * p.D;
-        float yv[2][4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float4 a = *reinterpret_cast<const float4*>(sY[uq][pl + e * L::ODD]);
-            const float4 u = *reinterpret_cast<const float4*>(sU[uq][pl + e * L::ODD]);
-            yv[e][0] = fmaf(feed[e], u.x, a.x); yv[e][1] = fmaf(feed[e], u.y, a.y);
-            yv[e][2] = fmaf(feed[e], u.z, a.z); yv[e][3] = fmaf(feed[e], u.w, a.w);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (!IN && tq + j >= end) continue;
-            if (z) {
-                const float2 g = Pair<T>::f(zc[j]);
-                yv[0][j] *= silu(g.x);
-                yv[1][j] *= silu(g.y);
+            for (int e = 0; e < 2; ++e) {
+                const float4 a = *reinterpret_cast<const float4*>(sY[tile & 1][uq][pl + e * L::ODD]);
+                const float4 u = *reinterpret_cast<const float4*>(sU[tile & 1][uq][pl + e * L::ODD]);
+                yv[e][0] = fmaf(feed[e], u.x, a.x); yv[e][1] = fmaf(feed[e], u.y, a.y);
+                yv[e][2] = fmaf(feed[e], u.z, a.z); yv[e][3] = fmaf(feed[e], u.w, a.w);
             }
-            stpair(yt + j * p.D + off, yv[0][j], yv[1][j]);
-        }
-    };
-    using Yes = std::true_type;
-    using No = std::false_type;
-    if (begin < end) fetch(begin, No());
-    const int place = L::place(ch);
-
-    for (int t0 = begin; t0 < end; t0 += kTile) {
-        const bool in = whole(t0);
-        if (in) stage(t0, Yes());
-        else stage(t0, No());
-        __syncthreads();
-        if (whole(t0 + kTile)) fetch(t0 + kTile, Yes());
-        else if (t0 + kTile < end) fetch(t0 + kTile, No());
-#pragma unroll 4
-        for (int q = 0; q < kTile / 4; ++q) {
-            if (!LOCAL && p.saved && (q & 3) == 0 && t0 + 4 * q < end) {
-                const size_t nc = (p.T + kSsmChunk - 1) / kSsmChunk;
-                const size_t at = (((size_t)bh * nc + (t0 + 4 * q) / kSsmChunk) * p.D + c0 + ch) * N + 4 * sl;
-                *reinterpret_cast<float4*>(p.saved + at) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
-            }
-            const float4 d4 = *reinterpret_cast<const float4*>(sD[q][place]);
-            const float4 u4 = *reinterpret_cast<const float4*>(sU[q][place]);
-            const float dd[4] = {d4.x, d4.y, d4.z, d4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
-            float yy[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const Quad bq = sB[4 * q + j][sl];
-                const float2 d2 = two(dd[j]), du = two(dd[j] * uu[j]);
-                s[0] = fma2(ex22(mul2(d2, A2[0])), s[0], mul2(du, Four<T>::lo(bq)));
-                s[1] = fma2(ex22(mul2(d2, A2[1])), s[1], mul2(du, Four<T>::hi(bq)));
-                if (LOCAL) {
-                    dsum += dd[j];
-                } else {
-                    const Quad cq = sC[4 * q + j][sl];
-                    const float2 v = fma2(s[1], Four<T>::hi(cq), mul2(s[0], Four<T>::lo(cq)));
-                    yy[j] = v.x + v.y;
+                if (!IN && tq + j >= end) continue;
+                if (z) {
+                    const float2 g = Pair<T>::f(zr[j]);
+                    yv[0][j] *= silu(g.x);
+                    yv[1][j] *= silu(g.y);
                 }
+                stpair(yt + j * p.D + off, yv[0][j], yv[1][j]);
             }
-            if (!LOCAL) {
-                const float r = lane_sum4<LPC>(yy[0], yy[1], yy[2], yy[3]);
-                if (sl < 4) sY[q][place][sl] = r;
+        };
+        using Yes = std::true_type;
+        using No = std::false_type;
+        auto fetch_any = [&](int tile) {
+            const int t0 = begin + tile * kTile;
+            if (!has_unit || tile >= tiles) return;
+            if (whole(t0)) fetch(t0, Yes());
+            else fetch(t0, No());
+        };
+        auto stage_any = [&](int tile) {
+            if (!has_unit || tile >= tiles) return;
+            if (whole(begin + tile * kTile)) stage(tile, Yes());
+            else stage(tile, No());
+        };
+        auto copy_any = [&](int tile) {
+            if (tile < tiles) copy_bc(tile);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        const bool out = !LOCAL && p.y && has_unit;
+        copy_any(0);
+        copy_any(1);
+        fetch_any(0);
+        stage_any(0);
+        fetch_any(1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        for (int k = 0; k <= tiles; ++k) {  // one turn more than the scan warps: the last tile's y
+            if (k > 0 && out) {
+                if (whole(begin + (k - 1) * kTile)) finish(k - 1, Yes());
+                else finish(k - 1, No());
+            }
+            if (k == tiles) break;
+            copy_any(k + 2);
+            stage_any(k + 1);
+            fetch_any(k + 2);
+            if (out && z) fetch_z(begin + k * kTile);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // B and C of tile k + 1 are there
+            __syncthreads();
+        }
+    } else {  // ------------------------------- scan warps
+        const int tid = threadIdx.x;
+        // states 4 sl .. 4 sl + 3 of channel ch
+        const int ch = tid / LPC, sl = tid % LPC, place = L::place(ch);
+        const size_t srow = ((size_t)bh * p.D + c0 + ch) * N + 4 * sl;
+        const size_t states = (size_t)p.B * p.H * p.D;
+        float2 A2[2], s[2] = {two(0.0f), two(0.0f)};
+        float dsum = 0.0f;
+        {
+            const float4 a = ld4(p.A + ((size_t)h * p.D + c0 + ch) * N + 4 * sl);
+            A2[0] = make_float2(a.x * kLog2e, a.y * kLog2e);
+            A2[1] = make_float2(a.z * kLog2e, a.w * kLog2e);
+        }
+        if (!LOCAL) {
+            if (p.S0) {
+                const float4 v = ld4(p.S0 + srow);
+                s[0] = make_float2(v.x, v.y);
+                s[1] = make_float2(v.z, v.w);
+            }
+            for (int j = 0; j < seg; ++j) {  // the segments before this one
+                const float4 v = *reinterpret_cast<const float4*>(sg.local + j * states * N + srow);
+                const float2 ds = two(sg.dsum[j * states + (size_t)bh * p.D + c0 + ch]);
+                s[0] = fma2(ex22(mul2(A2[0], ds)), s[0], make_float2(v.x, v.y));
+                s[1] = fma2(ex22(mul2(A2[1], ds)), s[1], make_float2(v.z, v.w));
             }
         }
         __syncthreads();
-        if (!LOCAL && p.y && has_unit) {
-            if (in) finish(t0, Yes());
-            else finish(t0, No());
+        for (int k = 0; k < tiles; ++k) {
+            const int t0 = begin + k * kTile, m = k & 1, m3 = k % 3;
+#pragma unroll 4
+            for (int q = 0; q < kTile / 4; ++q) {
+                if (!LOCAL && p.saved && (q & 3) == 0 && t0 + 4 * q < end) {
+                    const size_t nc = (p.T + kSsmChunk - 1) / kSsmChunk;
+                    const size_t at = (((size_t)bh * nc + (t0 + 4 * q) / kSsmChunk) * p.D + c0 + ch) * N + 4 * sl;
+                    *reinterpret_cast<float4*>(p.saved + at) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+                }
+                const float4 d4 = *reinterpret_cast<const float4*>(sD[m][q][place]);
+                const float4 u4 = *reinterpret_cast<const float4*>(sU[m][q][place]);
+                const float dd[4] = {d4.x, d4.y, d4.z, d4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
+                float yy[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const Quad bq = sB[m3][4 * q + j][sl];
+                    const float2 d2 = two(dd[j]), du = two(dd[j] * uu[j]);
+                    s[0] = fma2(ex22(mul2(d2, A2[0])), s[0], mul2(du, Four<T>::lo(bq)));
+                    s[1] = fma2(ex22(mul2(d2, A2[1])), s[1], mul2(du, Four<T>::hi(bq)));
+                    if (LOCAL) {
+                        dsum += dd[j];
+                    } else {
+                        const Quad cq = sC[m3][4 * q + j][sl];
+                        const float2 v = fma2(s[1], Four<T>::hi(cq), mul2(s[0], Four<T>::lo(cq)));
+                        yy[j] = v.x + v.y;
+                    }
+                }
+                if (!LOCAL) {
+                    const float r = lane_sum4<LPC>(yy[0], yy[1], yy[2], yy[3]);
+                    if (sl < 4) sY[m][q][place][sl] = r;
+                }
+            }
+            __syncthreads();
         }
-        // sU is written again by the threads that read it here; sY only behind the next barrier
+        if (LOCAL) {
+            *reinterpret_cast<float4*>(sg.local + seg * states * N + srow) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+            if (sl == 0) sg.dsum[seg * states + (size_t)bh * p.D + c0 + ch] = dsum;
+        } else if (end == len && p.ST) {
+            *reinterpret_cast<float4*>(p.ST + srow) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+        }
     }
-    if (LOCAL) {
-        const size_t states = (size_t)p.B * p.H * p.D;
-        *reinterpret_cast<float4*>(sg.local + seg * states * N + srow) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
-        if (sl == 0) sg.dsum[seg * states + (size_t)bh * p.D + c0 + ch] = dsum;
-        return;
-    }
-    if (!last) return;
-    if (p.ST) *reinterpret_cast<float4*>(p.ST + srow) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
-    if (p.cs_out) {  // the last W-1 inputs, some of them perhaps carried in
+    if (!LOCAL && end == len && p.cs_out) {  // the last W-1 inputs, some of them perhaps carried in
         T* out = static_cast<T*>(p.cs_out) + (size_t)bh * (p.W - 1) * p.D + c0;
-        for (int i = tid; i < (p.W - 1) * CPB; i += TH) {
+        for (int i = threadIdx.x; i < (p.W - 1) * CPB; i += TH + EW) {
             const int r = i / CPB, c = i % CPB, t = len - (p.W - 1) + r;
             float v = 0.0f;
             if (t >= 0) v = ldf(x + (size_t)t * p.D + c);
@@ -378,16 +421,26 @@ int segment_len(int T, int P) {
     return (tiles + P - 1) / P * kTile;
 }
 
-template <typename T, int N, int CPB>
-cudaError_t launch_fwd(const SsmParams& p, const SegArgs& sg, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((long long)p.B * p.H * (p.D / CPB));
-    if (sg.P > 1) {
-        ssm_fwd_kernel<T, N, CPB, true><<<dim3(blocks, sg.P - 1), CPB * N / 4, 0, s>>>(p, sg);
-        const cudaError_t e = cudaGetLastError();
+template <typename T, int N, int CPB, bool LOCAL>
+cudaError_t launch_fwd_pass(const SsmParams& p, const SegArgs& sg, cudaStream_t s) {
+    auto kern = ssm_fwd_kernel<T, N, CPB, LOCAL>;
+    constexpr int smem = sizeof(FwdSmem<T, N, CPB, LOCAL>);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    ssm_fwd_kernel<T, N, CPB, false><<<dim3(blocks, sg.P), CPB * N / 4, 0, s>>>(p, sg);
+    const dim3 grid((unsigned)((long long)p.B * p.H * (p.D / CPB)), LOCAL ? sg.P - 1 : sg.P);
+    kern<<<grid, CPB * N / 4 + kEw<CPB>, smem, s>>>(p, sg);
     return cudaGetLastError();
+}
+
+template <typename T, int N, int CPB>
+cudaError_t launch_fwd(const SsmParams& p, const SegArgs& sg, cudaStream_t s) {
+    if (sg.P > 1) {
+        const cudaError_t e = launch_fwd_pass<T, N, CPB, true>(p, sg, s);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_fwd_pass<T, N, CPB, false>(p, sg, s);
 }
 
 template <typename T>
