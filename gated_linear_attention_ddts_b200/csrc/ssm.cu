@@ -160,16 +160,26 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 2 
         auto stage = [&](int tile, auto inner) {
             constexpr bool IN = decltype(inner)::value;
             const int tq = begin + tile * kTile + 4 * uq;
-            float2 xv[7];
-#pragma unroll
-            for (int i = 0; i < 7; ++i) xv[i] = Pair<T>::f(xr[i]);
-            float du[2][4], uu[2][4];
+            // two neighbouring tokens of a channel an instruction
+            float2 d[2][2], u[2][2];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool live = IN || tq + j < end;
-                float2 d = Pair<T>::f(dr[j]);
-                float u0 = xv[3 + j].x, u1 = xv[3 + j].y;
-                if (p.W) {
+                const float2 a = Pair<T>::f(dr[j]);
+                (&d[0][j >> 1].x)[j & 1] = a.x;
+                (&d[1][j >> 1].x)[j & 1] = a.y;
+            }
+            if (p.preact) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) d[e][m] = softplus2(add2(d[e][m], two(bias[e])));
+            }
+            if (p.W) {
+                float2 xv[7];
+#pragma unroll
+                for (int i = 0; i < 7; ++i) xv[i] = Pair<T>::f(xr[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
                     float z0 = cb[0], z1 = cb[1];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -177,48 +187,65 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 2 
                             z0 = fmaf(w[i][0], xv[3 + j - i].x, z0);
                             z1 = fmaf(w[i][1], xv[3 + j - i].y, z1);
                         }
-                    u0 = p.silu ? silu(z0) : z0;
-                    u1 = p.silu ? silu(z1) : z1;
+                    (&u[0][j >> 1].x)[j & 1] = z0;
+                    (&u[1][j >> 1].x)[j & 1] = z1;
                 }
-                if (p.preact) {
-                    d.x = softplus(d.x + bias[0]);
-                    d.y = softplus(d.y + bias[1]);
+                if (p.silu) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) u[e][m] = silu2(u[e][m]);
                 }
-                // tokens behind the end leave the state as it is
-                du[0][j] = live ? d.x : 0.0f;
-                du[1][j] = live ? d.y : 0.0f;
-                uu[0][j] = live ? u0 : 0.0f;
-                uu[1][j] = live ? u1 : 0.0f;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 a = Pair<T>::f(xr[3 + j]);
+                    (&u[0][j >> 1].x)[j & 1] = a.x;
+                    (&u[1][j >> 1].x)[j & 1] = a.y;
+                }
+            }
+            if (!IN) {  // tokens behind the end leave the state as it is
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (tq + j >= end) (&d[e][j >> 1].x)[j & 1] = (&u[e][j >> 1].x)[j & 1] = 0.0f;
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int at = pl + e * L::ODD;
-                *reinterpret_cast<float4*>(sD[tile & 1][uq][at]) = make_float4(du[e][0], du[e][1], du[e][2], du[e][3]);
-                *reinterpret_cast<float4*>(sU[tile & 1][uq][at]) = make_float4(uu[e][0], uu[e][1], uu[e][2], uu[e][3]);
+                *reinterpret_cast<float4*>(sD[tile & 1][uq][at]) = make_float4(d[e][0].x, d[e][0].y, d[e][1].x, d[e][1].y);
+                *reinterpret_cast<float4*>(sU[tile & 1][uq][at]) = make_float4(u[e][0].x, u[e][0].y, u[e][1].x, u[e][1].y);
             }
         };
         auto finish = [&](int tile, auto inner) {  // y of the unit, with the skip and the gate
             constexpr bool IN = decltype(inner)::value;
             const int t0 = begin + tile * kTile, tq = t0 + 4 * uq;
             T* yt = y + (size_t)t0 * p.D;
-            float yv[2][4];
+            float2 yv[2][2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float4 a = *reinterpret_cast<const float4*>(sY[tile & 1][uq][pl + e * L::ODD]);
                 const float4 u = *reinterpret_cast<const float4*>(sU[tile & 1][uq][pl + e * L::ODD]);
-                yv[e][0] = fmaf(feed[e], u.x, a.x); yv[e][1] = fmaf(feed[e], u.y, a.y);
-                yv[e][2] = fmaf(feed[e], u.z, a.z); yv[e][3] = fmaf(feed[e], u.w, a.w);
+                yv[e][0] = fma2(two(feed[e]), make_float2(u.x, u.y), make_float2(a.x, a.y));
+                yv[e][1] = fma2(two(feed[e]), make_float2(u.z, u.w), make_float2(a.z, a.w));
+            }
+            if (z) {
+                float2 g[2][2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 a = Pair<T>::f(zr[j]);
+                    (&g[0][j >> 1].x)[j & 1] = a.x;
+                    (&g[1][j >> 1].x)[j & 1] = a.y;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) yv[e][m] = mul2(yv[e][m], silu2(g[e][m]));
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (!IN && tq + j >= end) continue;
-                if (z) {
-                    const float2 g = Pair<T>::f(zr[j]);
-                    yv[0][j] *= silu(g.x);
-                    yv[1][j] *= silu(g.y);
-                }
-                stpair(yt + j * p.D + off, yv[0][j], yv[1][j]);
-            }
+            for (int j = 0; j < 4; ++j)
+                if (IN || tq + j < end) stpair(yt + j * p.D + off, (&yv[0][j >> 1].x)[j & 1], (&yv[1][j >> 1].x)[j & 1]);
         };
         using Yes = std::true_type;
         using No = std::false_type;

@@ -8,32 +8,6 @@
 namespace rdm {
 namespace ssm {
 
-// softplus(x) = max(x, 0) + log1p(e^-|x|).  The steps sit near 1e-3..1e-1, where
-// the logarithm's argument is close to 1 and lg2.approx (absolute error 2^-22)
-// would leave only 12 of their bits; so log1p(y) = 2 atanh(s), s = y / (2 + y),
-// as 2 s P(s^2) with s^2 <= 1/9 (P fitted here, relative error 4e-9), which the
-// float32 states and gradients need.
-__device__ __forceinline__ float rcp_fast(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float softplus(float x) {
-    const float y = ex2_fast(-fabsf(x) * kLog2e);
-    const float s = y * rcp_fast(2.0f + y);
-    const float q = s * s;
-    float r = 0.2817833423614502f;
-    r = fmaf(r, q, 0.27960604429244995f);
-    r = fmaf(r, q, 0.40024909377098083f);
-    r = fmaf(r, q, 0.6666631698608398f);
-    r = fmaf(r, q, 2.0f);
-    return fmaf(s, r, fmaxf(x, 0.0f));  // NaN comes through s
-}
-__device__ __forceinline__ float sigmoid(float x) { return rcp_fast(1.0f + ex2_fast(-x * kLog2e)); }
-__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
-// d silu(x) / dx = s (1 + x (1 - s))
-__device__ __forceinline__ float dsilu(float x, float s) { return s * fmaf(x, 1.0f - s, 1.0f); }
-
 // Two float32 operations an instruction (sm_100's packed forms), each rounded as
 // the single one.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -49,8 +23,44 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
     return r;
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return r;
+}
 __device__ __forceinline__ float2 ex22(float2 x) { return make_float2(ex2_fast(x.x), ex2_fast(x.y)); }
 __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+
+// softplus(x) = max(x, 0) + log1p(e^-|x|).  The steps sit near 1e-3..1e-1, where
+// the logarithm's argument is close to 1 and lg2.approx (absolute error 2^-22)
+// would leave only 12 of their bits; so log1p(y) = 2 atanh(s), s = y / (2 + y),
+// as 2 s P(s^2) with s^2 <= 1/9 (P fitted here, relative error 4e-9), which the
+// float32 states and gradients need.
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 rcp2(float2 x) { return make_float2(rcp_fast(x.x), rcp_fast(x.y)); }
+__device__ __forceinline__ float2 softplus2(float2 x) {
+    const float2 y = ex22(make_float2(-fabsf(x.x) * kLog2e, -fabsf(x.y) * kLog2e));
+    const float2 s = mul2(y, rcp2(add2(y, two(2.0f))));
+    const float2 q = mul2(s, s);
+    float2 r = two(0.2817833423614502f);
+    r = fma2(r, q, two(0.27960604429244995f));
+    r = fma2(r, q, two(0.40024909377098083f));
+    r = fma2(r, q, two(0.6666631698608398f));
+    r = fma2(r, q, two(2.0f));
+    return fma2(s, r, make_float2(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f)));  // NaN comes through s
+}
+__device__ __forceinline__ float2 sigmoid2(float2 x) { return rcp2(add2(ex22(mul2(x, two(-kLog2e))), two(1.0f))); }
+__device__ __forceinline__ float2 silu2(float2 x) { return mul2(x, sigmoid2(x)); }
+__device__ __forceinline__ float softplus(float x) { return softplus2(two(x)).x; }
+__device__ __forceinline__ float sigmoid(float x) { return rcp_fast(1.0f + ex2_fast(-x * kLog2e)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+// d silu(x) / dx = s (1 + x (1 - s))
+__device__ __forceinline__ float dsilu(float x, float s) { return s * fmaf(x, 1.0f - s, 1.0f); }
 
 // Two neighbouring channels of a row.
 template <typename T>
