@@ -32,11 +32,6 @@ namespace {
 using tc::unpack8;
 
 // ------------------------------------------------------------------ rounding a block
-__device__ __forceinline__ float finite_abs(float x) {
-    const float a = fabsf(x);
-    return a <= 3.4e38f ? a : 0.0f;  // neither infinite nor NaN (bf16 ends at 3.39e38)
-}
-
 // The scale of a block whose largest magnitude is `most`; 1 for a block of zeros.
 template <bool I8>
 __device__ __forceinline__ float block_scale(float most) {
@@ -48,91 +43,211 @@ __device__ __forceinline__ float block_scale(float most) {
     return __uint_as_float((unsigned)(max(e, -126) + 127) << 23);
 }
 
-template <bool I8>
-__device__ __forceinline__ unsigned char encode(float x, float scale, float inv) {
-    if (I8) return (unsigned char)(signed char)max(-127, min(127, __float2int_rn(__fdiv_rn(x, scale))));
-    return __nv_cvt_float_to_fp8(x * inv, __NV_SATFINITE, __NV_E4M3);
+// Four values as codes.  int8 rounds x / scale; x times the rounded reciprocal is
+// within 3 2^-24 of that quotient (relative), 3e-5 at most below 128, so only next
+// to a border between two codes does the division itself have to decide (`exact`:
+// for all, where values or the reciprocal are not finite).  Adding 1.5 2^23 rounds
+// to nearest even and leaves the code in the low byte.
+__device__ __noinline__ uint32_t int8_codes(float4 x, float scale) {
+    auto code = [&](float v) { return (uint32_t)(max(-127, min(127, __float2int_rn(__fdiv_rn(v, scale)))) & 0xff); };
+    return code(x.x) | code(x.y) << 8 | code(x.z) << 16 | code(x.w) << 24;
 }
+template <bool I8>
+__device__ __forceinline__ uint32_t encode4(const float* x, float scale, float inv, bool exact) {
+    if (!I8) {
+        const unsigned lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const unsigned hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
+        return lo | hi << 16;
+    }
+    uint32_t u[4];
+    float off = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float t = x[e] * inv, r = t + 12582912.0f;
+        u[e] = __float_as_uint(r);
+        off = fmaxf(off, fabsf(t - (r - 12582912.0f)));
+    }
+    if (exact || off > 0.4999f) return int8_codes(make_float4(x[0], x[1], x[2], x[3]), scale);
+    return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+}
+
+// The larger magnitude of each half of two bf16 pairs, as bits: those of values
+// that are not finite are 0x7f80 and above.
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint4 v) {
+    m = __vmaxu2(m, v.x & 0x7fff7fffu);
+    m = __vmaxu2(m, v.y & 0x7fff7fffu);
+    m = __vmaxu2(m, v.z & 0x7fff7fffu);
+    return __vmaxu2(m, v.w & 0x7fff7fffu);
+}
+__device__ __forceinline__ uint32_t warp_max_bits(uint32_t m) {
+    const uint32_t x = max(m & 0xffffu, m >> 16);
+    return __reduce_max_sync(0xffffffffu, x);
+}
+// The largest finite magnitude among pieces i, i + step, ... below n of a block.
+__device__ __noinline__ uint32_t finite_bits(const uint4* src, int i, int step, int n) {
+    uint32_t m = 0;
+    for (; i < n; i += step) {
+        const uint4 v = src[i];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t b = (w[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+            if (b < 0x7f80u) m = max(m, b);
+        }
+    }
+    return m;
+}
+// `m` and the bits as a value: the block's largest finite magnitude.
+__device__ __forceinline__ float bits_value(uint32_t m) { return __uint_as_float(m << 16); }
 
 constexpr int kThreads = 128;
 
 // Rounds `rows` rows of D values (row r at src + r * D) into dst and *scale, by
-// the whole CTA.
-template <bool I8, int D>
+// the whole CTA of TH threads; at most 64 rows, read once and kept in registers.
+template <bool I8, int D, int TH>
 __device__ void round_block(const __nv_bfloat16* src, int rows, unsigned char* dst, float* scale) {
-    __shared__ float red[32];
+    __shared__ uint32_t red[2][TH / 32];
+    constexpr int K = 64 * (D / 8) / TH;
     const int n8 = rows * (D / 8);
-    float most = 0.0f;
-    for (int i = threadIdx.x; i < n8; i += blockDim.x) {
-        float f[8];
-        unpack8(reinterpret_cast<const uint4*>(src)[i], f);
+    uint4 v[K];
+    uint32_t most = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most = fmaxf(most, finite_abs(f[e]));
+    for (int k = 0; k < K; ++k) {
+        const int i = threadIdx.x + k * TH;
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (i < n8) v[k] = reinterpret_cast<const uint4*>(src)[i];
+        most = max_bits(most, v[k]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = most;
+    most = warp_max_bits(most);
+    if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = most;
     __syncthreads();
-    most = red[0];
-    for (int w = 1; w < (int)blockDim.x / 32; ++w) most = fmaxf(most, red[w]);
-    const float s = block_scale<I8>(most), inv = I8 ? 0.0f : __fdiv_rn(1.0f, s);
-    for (int i = threadIdx.x; i < n8; i += blockDim.x) {
-        float f[8];
-        unpack8(reinterpret_cast<const uint4*>(src)[i], f);
-        uint32_t w[2] = {0, 0};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)encode<I8>(f[e], s, inv) << (8 * (e & 3));
-        reinterpret_cast<uint2*>(dst)[i] = make_uint2(w[0], w[1]);
+    for (int w = 0; w < TH / 32; ++w) most = max(most, red[0][w]);
+    const bool odd = most >= 0x7f80u;
+    if (odd) {
+        most = __reduce_max_sync(0xffffffffu, finite_bits(reinterpret_cast<const uint4*>(src), threadIdx.x, TH, n8));
+        if ((threadIdx.x & 31) == 0) red[1][threadIdx.x >> 5] = most;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < TH / 32; ++w) most = max(most, red[1][w]);
+    }
+    const float s = block_scale<I8>(bits_value(most)), inv = __fdiv_rn(1.0f, s);
+    const bool exact = odd || !(inv < INFINITY);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = threadIdx.x + k * TH;
+        if (i >= n8) break;
+        float f[8];
+        unpack8(v[k], f);
+        reinterpret_cast<uint2*>(dst)[i] = make_uint2(encode4<I8>(f, s, inv, exact), encode4<I8>(f + 4, s, inv, exact));
     }
     if (threadIdx.x == 0) *scale = s;
     __syncthreads();
 }
 
 // ------------------------------------------------------------------ fill from a prompt
-// One CTA per (block of slots, sequence, head; the shared key counts as a head).
-template <bool I8, int D>
-__device__ void fill_block(const SkaQ8FillParams& p, const __nv_bfloat16* src, int blk, int len, unsigned char* dst,
-                           float* scale, __nv_bfloat16* tail) {
-    const int w = p.c.window, R = p.c.block;
+// One to four warps a block (64 values a lane), all of a block's rows in registers
+// between the search for its largest magnitude and the rounding: each value is
+// read once.  kThreads / 32 warps a CTA, on neighbouring blocks of one head.
+template <int D, int R>
+constexpr int kBlockWarps = R * D <= 2048 ? 1 : R * D / 2048;
+
+template <bool I8, int D, int R>
+__device__ void fill_blocks(const SkaQ8Cache& c, const __nv_bfloat16* src, int first, int len, unsigned char* dst,
+                            float* scale, __nv_bfloat16* tail) {
+    constexpr int WPB = kBlockWarps<D, R>, K = R * (D / 8) / (32 * WPB);
+    __shared__ uint32_t red[2][kThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, idx = (warp % WPB) * 32 + lane;
+    const int blk = first + warp / WPB, w = c.window;
     const int at = blk * R, stop = min(at + R, w);
-    const int last = len - 1, round = last / w, cur = last % w;
-    int r = round;  // the last round in which the block became full
-    if (cur < stop - 1) --r;
+    const int last = len - 1, cur = last % w;
+    int round = last / w;  // the last round in which the block became full
     if (at <= cur && cur < stop - 1) {  // the block being written
         const __nv_bfloat16* s = src + ((size_t)round * w + at) * D;
-        for (int i = threadIdx.x; i < (cur - at + 1) * (D / 8); i += kThreads)
+        for (int i = idx; i < (cur - at + 1) * (D / 8); i += 32 * WPB)
             reinterpret_cast<uint4*>(tail)[i] = reinterpret_cast<const uint4*>(s)[i];
     }
-    if (r < 0) return;
-    round_block<I8, D>(src + ((size_t)r * w + at) * D, stop - at, dst + (size_t)at * D, scale + blk);
+    if (cur < stop - 1) --round;
+    const int n8 = at < w && round >= 0 ? (stop - at) * (D / 8) : 0;
+    const uint4* s4 = reinterpret_cast<const uint4*>(src + ((size_t)max(round, 0) * w + at) * D);
+    uint4 v[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = idx + k * 32 * WPB;
+        v[k] = i < n8 ? __ldg(s4 + i) : make_uint4(0, 0, 0, 0);
+    }
+    uint32_t most = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) most = max_bits(most, v[k]);
+    most = warp_max_bits(most);
+    auto join = [&](int turn) {  // over the block's warps
+        if (WPB == 1) return;
+        if (lane == 0) red[turn][warp] = most;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < WPB; ++k) most = max(most, red[turn][warp / WPB * WPB + k]);
+    };
+    join(0);
+    const bool odd = most >= 0x7f80u;
+    if (WPB == 1 ? odd : __syncthreads_or(odd)) {
+        if (odd) most = __reduce_max_sync(0xffffffffu, finite_bits(s4, idx, 32 * WPB, n8));
+        join(1);
+    }
+    if (n8 == 0) return;
+    const float s = block_scale<I8>(bits_value(most)), inv = __fdiv_rn(1.0f, s);
+    const bool exact = odd || !(inv < INFINITY);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = idx + k * 32 * WPB;
+        if (i >= n8) break;
+        float f[8];
+        unpack8(v[k], f);
+        reinterpret_cast<uint2*>(dst + (size_t)at * D)[i] = make_uint2(encode4<I8>(f, s, inv, exact), encode4<I8>(f + 4, s, inv, exact));
+    }
+    if (idx == 0) scale[blk] = s;
 }
 
-template <bool I8>
+template <int D, int R>
+__host__ __device__ constexpr int blocks_per_cta() {
+    return kThreads / 32 / kBlockWarps<D, R>;
+}
+// CTAs that a row of nb blocks takes.
+template <int R>
+__host__ __device__ inline int row_ctas(int d, int nb) {
+    const int per = d == 64 ? blocks_per_cta<64, R>() : blocks_per_cta<128, R>();
+    return (nb + per - 1) / per;
+}
+
+template <bool I8, int R>
 __global__ void __launch_bounds__(kThreads) ska_q8_fill_kernel(const SkaQ8FillParams p) {
     const SkaQ8Cache& c = p.c;
-    const int nb = (c.window + c.block - 1) / c.block;
-    const int blk = blockIdx.x % nb, row = blockIdx.x / nb, b = row / (c.H + 1), h = row % (c.H + 1) - 1;
+    const int nb = (c.window + R - 1) / R;
+    const int kctas = row_ctas<R>(c.dk, nb), vctas = row_ctas<R>(c.dv, nb);
+    const int per = kctas + c.H * vctas, b = blockIdx.x / per, i = blockIdx.x % per;
     int len = p.lengths ? p.lengths[b] : p.T;
     if (len < 0 || len > p.T) {
         if (threadIdx.x == 0) atomicOr(p.err, kErrBadValue);
         len = len < 0 ? 0 : p.T;
     }
-    if (blk == 0 && h < 0 && threadIdx.x == 0) c.pos[b] = len;
+    if (i == 0 && threadIdx.x == 0) c.pos[b] = len;
     if (len == 0) return;
-    if (h < 0) {
+    if (i < kctas) {
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.k) + (size_t)b * p.T * c.dk;
         unsigned char* dst = c.k + (size_t)b * c.window * c.dk;
-        __nv_bfloat16* tail = static_cast<__nv_bfloat16*>(c.k_tail) + (size_t)b * c.block * c.dk;
-        if (c.dk == 64) fill_block<I8, 64>(p, src, blk, len, dst, c.k_scale + (size_t)b * nb, tail);
-        else fill_block<I8, 128>(p, src, blk, len, dst, c.k_scale + (size_t)b * nb, tail);
+        __nv_bfloat16* tail = static_cast<__nv_bfloat16*>(c.k_tail) + (size_t)b * R * c.dk;
+        float* scale = c.k_scale + (size_t)b * nb;
+        if (c.dk == 64) fill_blocks<I8, 64, R>(c, src, i * blocks_per_cta<64, R>(), len, dst, scale, tail);
+        else fill_blocks<I8, 128, R>(c, src, i * blocks_per_cta<128, R>(), len, dst, scale, tail);
         return;
     }
+    const int h = (i - kctas) / vctas, j = (i - kctas) % vctas;
     const size_t bh = (size_t)b * c.H + h;
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.v) + bh * p.T * c.dv;
     unsigned char* dst = c.v + bh * c.window * c.dv;
-    __nv_bfloat16* tail = static_cast<__nv_bfloat16*>(c.v_tail) + bh * c.block * c.dv;
-    if (c.dv == 64) fill_block<I8, 64>(p, src, blk, len, dst, c.v_scale + bh * nb, tail);
-    else fill_block<I8, 128>(p, src, blk, len, dst, c.v_scale + bh * nb, tail);
+    __nv_bfloat16* tail = static_cast<__nv_bfloat16*>(c.v_tail) + bh * R * c.dv;
+    float* scale = c.v_scale + bh * nb;
+    if (c.dv == 64) fill_blocks<I8, 64, R>(c, src, j * blocks_per_cta<64, R>(), len, dst, scale, tail);
+    else fill_blocks<I8, 128, R>(c, src, j * blocks_per_cta<128, R>(), len, dst, scale, tail);
 }
 
 // ------------------------------------------------------------------ one token
@@ -161,6 +276,11 @@ __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a <= 3.4e38f ? a : 0.0f;  // neither infinite nor NaN (bf16 ends at 3.39e38)
 }
 
 // Four codes as two f16 pairs.
@@ -480,9 +600,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
         if (cur == w - 1 || fill == R - 1) {
             __syncthreads();
             if (group == 0)
-                round_block<I8, DK>(kt, fill + 1, c.k + ((size_t)b * w + at) * DK, c.k_scale + (size_t)b * nb + at / R);
+                round_block<I8, DK, kDecThreads>(kt, fill + 1, c.k + ((size_t)b * w + at) * DK, c.k_scale + (size_t)b * nb + at / R);
             for (int hh = 0; hh < nh; ++hh)
-                round_block<I8, DV>(vt + (size_t)hh * R * DV, fill + 1, c.v + ((bh0 + hh) * w + at) * DV,
+                round_block<I8, DV, kDecThreads>(vt + (size_t)hh * R * DV, fill + 1, c.v + ((bh0 + hh) * w + at) * DV,
                                     c.v_scale + (bh0 + hh) * nb + at / R);
         }
     }
@@ -613,12 +733,22 @@ cudaError_t launch_decode_t(const SkaQ8DecodeParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_ska_q8_fill(const SkaQ8FillParams& p, cudaStream_t s) {
-    const int nb = (p.c.window + p.c.block - 1) / p.c.block;
-    const unsigned grid = (unsigned)((long long)nb * p.c.B * (p.c.H + 1));
-    if (p.c.int8) ska_q8_fill_kernel<true><<<grid, kThreads, 0, s>>>(p);
-    else ska_q8_fill_kernel<false><<<grid, kThreads, 0, s>>>(p);
+namespace {
+template <bool I8, int R>
+cudaError_t launch_fill(const SkaQ8FillParams& p, cudaStream_t s) {
+    const int nb = (p.c.window + R - 1) / R;
+    const long long grid = p.c.B * (row_ctas<R>(p.c.dk, nb) + (long long)p.c.H * row_ctas<R>(p.c.dv, nb));
+    ska_q8_fill_kernel<I8, R><<<(unsigned)grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_ska_q8_fill(const SkaQ8FillParams& p, cudaStream_t s) {
+    switch (p.c.block) {
+        case 16: return p.c.int8 ? launch_fill<true, 16>(p, s) : launch_fill<false, 16>(p, s);
+        case 32: return p.c.int8 ? launch_fill<true, 32>(p, s) : launch_fill<false, 32>(p, s);
+        default: return p.c.int8 ? launch_fill<true, 64>(p, s) : launch_fill<false, 64>(p, s);
+    }
 }
 
 size_t ska_q8_decode_workspace(const SkaQ8DecodeParams& p) { return plan_bytes(p, plan(p)); }

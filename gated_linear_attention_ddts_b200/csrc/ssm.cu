@@ -366,62 +366,116 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 2 
 }
 
 // ------------------------------------------------------------------ single tokens
-constexpr int kStepThreads = 128;
+constexpr int kStepThreads = 256;
 
-// One thread has four states of a channel; a channel's lanes share its inputs.
-// A pure stream of the state, read and written once.
-template <typename T, int N>
+// A block has 1024 / N channels of R sequences, four states a thread; one read of A
+// serves the R sequences.  A stream of the state, read and written once.  One
+// thread per channel and sequence makes delta, u and the gate while the states are
+// on their way (in the first version every lane of a channel did, and the loads of
+// the 16 or 32 of them bounded it: B256 H16 D128 N64 142 us); its inputs, B and C
+// are asked for before the states, so that nothing waits behind them.
+template <typename T, int N, int R>
 __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmStepParams p) {
-    constexpr int LPC = N / 4;
-    const size_t i = (size_t)blockIdx.x * kStepThreads + threadIdx.x;
-    const size_t rows = (size_t)p.B * p.H * p.D;
-    const bool live = i / LPC < rows;
-    const size_t row = live ? i / LPC : rows - 1;  // idle lanes follow the last channel and store nothing
-    const int sl = (int)(i % LPC);
-    const int c = (int)(row % p.D);
-    const int bh = (int)(row / p.D), b = bh / p.H, h = bh % p.H;
-    const int hc = h * p.D + c;
-    const float4 s4 = *reinterpret_cast<const float4*>(p.S + row * N + 4 * sl);
-    const float4 a4 = ld4(p.A + (size_t)hc * N + 4 * sl);
-    const size_t grow = (size_t)(b * p.G + h / (p.H / p.G)) * N + 4 * sl;
-    const float4 b4 = ld4(static_cast<const T*>(p.Bm) + grow), c4 = ld4(static_cast<const T*>(p.Cm) + grow);
-    const T* x = static_cast<const T*>(p.x);
-    float u = ldf(x + row), d = ldf(static_cast<const T*>(p.dt) + row);
-    if (p.W) {
-        T* cs = static_cast<T*>(p.cs) + (size_t)bh * (p.W - 1) * p.D + c;
-        const T xt = x[row];
-        T old[3];
-        float acc = fmaf(p.cw[(size_t)hc * p.W], u, p.cb ? p.cb[hc] : 0.0f);
+    constexpr int LPC = N / 4, CB = kStepThreads / LPC, ITEMS = (R * CB + kStepThreads - 1) / kStepThreads;
+    constexpr int HB = CB <= 16 ? 1 : CB / 16;  // heads a block may reach into (D >= 16)
+    constexpr int QUADS = R * HB * LPC, BCQ = (QUADS + kStepThreads - 1) / kStepThreads;
+    using Quad = typename Four<T>::Raw;
+    __shared__ float4 sm[R][CB];  // delta, u, factor of the output, skip
+    __shared__ __align__(16) Quad sB[QUADS];
+    __shared__ __align__(16) Quad sC[QUADS];
+    const int ds = 31 - __clz(p.D), hd = p.H << ds, nblk = (hd + CB - 1) / CB, hpg = p.H / p.G;
+    const int first = (blockIdx.x % nblk) * CB, b0 = (blockIdx.x / nblk) * R, h0 = first >> ds;
+    const int tid = threadIdx.x, ch = tid / LPC, sl = tid % LPC;
+    const int hc = first + ch, hcc = min(hc, hd - 1);  // threads without a channel follow the last one and store nothing
+    // ---- ask for everything
+    float xv[ITEMS], dv[ITEMS], zv[ITEMS];
+    T raw[ITEMS], old[ITEMS][3];
 #pragma unroll
-        for (int k = 1; k < 4; ++k)
-            if (k < p.W) {
-                old[k - 1] = cs[(size_t)(p.W - 1 - k) * p.D];
-                acc = fmaf(p.cw[(size_t)hc * p.W + k], ldf(&old[k - 1]), acc);
+    for (int m = 0; m < ITEMS; ++m) {
+        const int i = tid + m * kStepThreads, r = i / CB, k = first + i % CB, b = b0 + r;
+        xv[m] = dv[m] = zv[m] = 0.0f;
+        if (r < R && k < hd && b < p.B) {
+            const size_t row = (size_t)b * hd + k;
+            raw[m] = static_cast<const T*>(p.x)[row];
+            dv[m] = ldf(static_cast<const T*>(p.dt) + row);
+            if (p.z) zv[m] = ldf(static_cast<const T*>(p.z) + row);
+            if (p.W > 1) {
+                const T* cs = static_cast<const T*>(p.cs) + ((((size_t)b * p.H + (k >> ds)) * (p.W - 1)) << ds) + (k & (p.D - 1));
+#pragma unroll
+                for (int j = 1; j < 4; ++j)
+                    if (j < p.W) old[m][j - 1] = cs[(size_t)(p.W - 1 - j) << ds];
             }
-        u = p.silu ? silu(acc) : acc;
-        __syncwarp();  // every lane of the channel has read the old inputs
-        if (sl == 0 && live) {
-            if (p.W > 1) cs[(size_t)(p.W - 2) * p.D] = xt;
-#pragma unroll
-            for (int k = 1; k < 3; ++k)
-                if (k < p.W - 1) cs[(size_t)(p.W - 2 - k) * p.D] = old[k - 1];
         }
     }
-    if (p.preact) d = softplus(d + (p.dt_bias ? p.dt_bias[hc] : 0.0f));
-    const float d2 = d * kLog2e, du = d * u;
-    float4 s;
-    s.x = fmaf(ex2_fast(d2 * a4.x), s4.x, du * b4.x);
-    s.y = fmaf(ex2_fast(d2 * a4.y), s4.y, du * b4.y);
-    s.z = fmaf(ex2_fast(d2 * a4.z), s4.z, du * b4.z);
-    s.w = fmaf(ex2_fast(d2 * a4.w), s4.w, du * b4.w);
-    if (live) *reinterpret_cast<float4*>(p.S + row * N + 4 * sl) = s;
-    float y = fmaf(s.x, c4.x, fmaf(s.y, c4.y, fmaf(s.z, c4.z, s.w * c4.w)));
+    Quad bq[BCQ], cq[BCQ];
 #pragma unroll
-    for (int o = 1; o < LPC; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (sl == 0 && live) {
-        if (p.dfeed) y = fmaf(p.dfeed[hc], u, y);
-        if (p.z) y *= silu(ldf(static_cast<const T*>(p.z) + row));
-        stf(static_cast<T*>(p.y) + row, y);
+    for (int m = 0; m < BCQ; ++m) {
+        const int i = tid + m * kStepThreads, n = i % LPC, hh = i / LPC % HB, r = i / LPC / HB;
+        if (i < QUADS) {
+            const size_t at = ((size_t)min(b0 + r, p.B - 1) * p.G + min(h0 + hh, p.H - 1) / hpg) * N + 4 * n;
+            bq[m] = Four<T>::ld(static_cast<const T*>(p.Bm) + at);
+            cq[m] = Four<T>::ld(static_cast<const T*>(p.Cm) + at);
+        }
+    }
+    float* S = p.S + ((size_t)b0 * hd + hcc) * N + 4 * sl;
+    const size_t next = (size_t)hd * N;
+    float4 s4[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s4[r] = *reinterpret_cast<const float4*>(S + (b0 + r < p.B ? r * next : 0));
+    const float4 a4 = ld4(p.A + (size_t)hcc * N + 4 * sl);
+    // ---- per channel and sequence
+#pragma unroll
+    for (int m = 0; m < ITEMS; ++m) {
+        const int i = tid + m * kStepThreads, r = i / CB, k = first + i % CB, b = b0 + r;
+        if (r < R && k < hd && b < p.B) {
+            float u = ldf(&raw[m]), d = dv[m];
+            if (p.W) {
+                float acc = fmaf(p.cw[(size_t)k * p.W], u, p.cb ? p.cb[k] : 0.0f);
+                T* cs = static_cast<T*>(p.cs) + ((((size_t)b * p.H + (k >> ds)) * (p.W - 1)) << ds) + (k & (p.D - 1));
+#pragma unroll
+                for (int j = 1; j < 4; ++j)
+                    if (j < p.W) {
+                        acc = fmaf(p.cw[(size_t)k * p.W + j], ldf(&old[m][j - 1]), acc);
+                        cs[(size_t)(p.W - 1 - j) << ds] = j == 1 ? raw[m] : old[m][j > 1 ? j - 2 : 0];
+                    }
+                u = p.silu ? silu(acc) : acc;
+            }
+            if (p.preact) d = softplus(d + (p.dt_bias ? p.dt_bias[k] : 0.0f));
+            sm[r][i % CB] = make_float4(d, u, p.z ? silu(zv[m]) : 1.0f, p.dfeed ? p.dfeed[k] * u : 0.0f);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < BCQ; ++m) {
+        const int i = tid + m * kStepThreads;
+        if (i < QUADS) {
+            sB[i] = bq[m];
+            sC[i] = cq[m];
+        }
+    }
+    __syncthreads();
+    // ---- the states
+    const float2 A2[2] = {make_float2(a4.x * kLog2e, a4.y * kLog2e), make_float2(a4.z * kLog2e, a4.w * kLog2e)};
+    const int hh = (hcc >> ds) - h0;
+#pragma unroll
+    for (int q = 0; q < R; q += 4) {
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int r = q; r < R && r < q + 4; ++r) {
+            const float4 v = sm[r][ch];
+            const Quad bb = sB[(r * HB + hh) * LPC + sl], cc = sC[(r * HB + hh) * LPC + sl];
+            const float2 d2 = two(v.x), du = two(v.x * v.y);
+            const float2 lo = fma2(ex22(mul2(d2, A2[0])), make_float2(s4[r].x, s4[r].y), mul2(du, Four<T>::lo(bb)));
+            const float2 hi = fma2(ex22(mul2(d2, A2[1])), make_float2(s4[r].z, s4[r].w), mul2(du, Four<T>::hi(bb)));
+            const float2 t = fma2(hi, Four<T>::hi(cc), mul2(lo, Four<T>::lo(cc)));
+            y[r - q] = t.x + t.y;
+            if (hc < hd && b0 + r < p.B) *reinterpret_cast<float4*>(S + r * next) = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
+        const float sum = lane_sum4<LPC>(y[0], y[1], y[2], y[3]);  // lane sl < 4 has sequence q + sl's
+        const int r = q + sl;
+        if (sl < 4 && r < R && hc < hd && b0 + r < p.B) {
+            const float4 v = sm[r][ch];
+            stf(static_cast<T*>(p.y) + (size_t)(b0 + r) * hd + hc, (sum + v.w) * v.z);
+        }
     }
 }
 
@@ -480,17 +534,28 @@ cudaError_t launch_fwd_t(const SsmParams& p, const SegArgs& sg, cudaStream_t s) 
     }
 }
 
+template <typename T, int N>
+cudaError_t launch_step(const SsmStepParams& p, cudaStream_t s) {
+    constexpr int CB = kStepThreads / (N / 4);
+    const long long nblk = ((long long)p.H * p.D + CB - 1) / CB;
+    // Eight sequences a block where that leaves every SM eight blocks (one read of A
+    // for eight states, and 128 bytes a thread on their way), else one, so that the
+    // few blocks spread over the SMs.
+    const bool many = nblk * ((p.B + 7) / 8) >= 8LL * sm_count();
+    const long long grid = nblk * (many ? (p.B + 7) / 8 : p.B);
+    if (many) ssm_step_kernel<T, N, 8><<<(unsigned)grid, kStepThreads, 0, s>>>(p);
+    else ssm_step_kernel<T, N, 1><<<(unsigned)grid, kStepThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_step_t(const SsmStepParams& p, cudaStream_t s) {
-    const long long threads = (long long)p.B * p.H * p.D * (p.N / 4);
-    const unsigned grid = (unsigned)((threads + kStepThreads - 1) / kStepThreads);
     switch (p.N) {
-        case 16: ssm_step_kernel<T, 16><<<grid, kStepThreads, 0, s>>>(p); break;
-        case 32: ssm_step_kernel<T, 32><<<grid, kStepThreads, 0, s>>>(p); break;
-        case 64: ssm_step_kernel<T, 64><<<grid, kStepThreads, 0, s>>>(p); break;
-        default: ssm_step_kernel<T, 128><<<grid, kStepThreads, 0, s>>>(p); break;
+        case 16: return launch_step<T, 16>(p, s);
+        case 32: return launch_step<T, 32>(p, s);
+        case 64: return launch_step<T, 64>(p, s);
+        default: return launch_step<T, 128>(p, s);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace
