@@ -265,7 +265,46 @@ __global__ void __launch_bounds__(kThreads) ska_q8_fill_kernel(const SkaQ8FillPa
 // them each byte of V costs 0.25 byte permutations, half a conversion and 1/256 of
 // an mma a warp, and the sweep stays bound by HBM.
 // The tail's slots go through the same steps in bf16, the weights in three parts.
-constexpr int kWarps = 8, kDecThreads = 32 * kWarps, kChunk = 512, kStride = kChunk + 4;
+// Each warp's tiles (the keys', then the values' of its head) come through a ring
+// of its own, four tiles ahead, so that 64 KB a CTA are on their way in every phase;
+// with loads into registers two tiles ahead and nothing in flight between the
+// phases HBM ran at 37% (B256 H16 d128 window 512: 106 us against XXX).
+constexpr int kWarps = 8, kDecThreads = 32 * kWarps, kChunk = 512, kStride = kChunk + 4, kRing = 4;
+
+template <int DK, int DV>
+struct Q8Smem {
+    uint4 ring[kWarps][kRing][16 * (DK > DV ? DK : DV) / 16];
+    float sc[kWarps][kStride];
+    __half wt[kWarps][2][kChunk];
+    __nv_bfloat16 qs[kWarps][DK];
+    float part[kWarps][DV];
+    float stat[kWarps][3];
+};
+
+// Place of 16-byte piece x of row r in a tile of 16 rows, such that the lanes that
+// read together (KEYS: rows g and pieces l4; else rows 2 l4 and pieces by g) spread
+// over the banks.
+template <int D, bool KEYS>
+__device__ __forceinline__ int tile_place(int r, int x) {
+    if (D == 128) return r * 8 + (KEYS ? x ^ ((r & 1) << 2) : x ^ (((r >> 1) & 3) << 1));
+    const int line = r >> 1, at = (r & 1) * 4 + x;
+    return line * 8 + (KEYS ? at : at ^ ((line & 3) << 1));
+}
+
+// Starts the copy of rows t0 .. t0 + 15, those outside [lo, hi) as the nearest inside.
+template <int D, bool KEYS>
+__device__ __forceinline__ void copy_tile(uint4* dst, const unsigned char* base, int t0, int lo, int hi) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+        const int i = lane + 32 * j, r = i / (D / 16), x = i % (D / 16);
+        const int u = min(max(t0 + r, lo), hi - 1);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         (unsigned)__cvta_generic_to_shared(dst + tile_place<D, KEYS>(r, x))),
+                     "l"(base + (size_t)u * D + 16 * x)
+                     : "memory");
+    }
+}
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -315,11 +354,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
     constexpr int KW = DK / 16;    // words of codes a lane has of a key row
     constexpr int VB = DV / 8;     // value columns a lane has
     constexpr int MT = DV / 16;    // value tiles of 16 columns
-    __shared__ __align__(16) float sc[kWarps][kStride];
-    __shared__ __align__(16) __half wt[kWarps][2][kChunk];
-    __shared__ __align__(16) __nv_bfloat16 qs[kWarps][DK];
-    __shared__ float part[kWarps][DV];
-    __shared__ float stat[kWarps][3];
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Q8Smem<DK, DV>& sm = *reinterpret_cast<Q8Smem<DK, DV>*>(smem_raw);
+    auto& sc = sm.sc;
+    auto& wt = sm.wt;
+    auto& qs = sm.qs;
+    auto& part = sm.part;
+    auto& stat = sm.stat;
     const SkaQ8Cache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, l4 = lane & 3;
     const int group = blockIdx.x % pl.groups, b = blockIdx.x / pl.groups, split = blockIdx.y;
@@ -351,7 +392,51 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
 
+    // This warp's tiles in the order in which it takes them: of each chunk first the
+    // keys' (16 slots each, every eighth tile), then the values'.
+    int pc = s0, pk = 0, pv = 0, slot_in = 0, slot_out = 0;  // the next to ask for, ring places
+    auto bounds = [&](int t0, int end, int& lo, int& hi) {  // slots of a tile that are in the cache
+        lo = (t0 & ~(R - 1)) == at ? max(t0, cur + 1) : t0;
+        hi = min(t0 + 16, end);
+    };
+    auto ask = [&]() {
+        while (pc < s1) {
+            const int c1 = min(pc + kChunk, s1);
+            int t0 = pc + 16 * (warp + kWarps * pk);
+            const bool key = t0 < c1;
+            if (!key) t0 = pc + 16 * (sub + wph * pv);
+            if (!key && (!busy || t0 >= c1)) {
+                pc += kChunk;
+                pk = pv = 0;
+                continue;
+            }
+            int lo, hi;
+            bounds(t0, c1, lo, hi);
+            if (lo >= hi) lo = t0, hi = c1;  // none of them: copied and not used
+            uint4* dst = sm.ring[warp][slot_in];
+            if (key) {
+                copy_tile<DK, true>(dst, kc, t0, lo, hi);
+                ++pk;
+            } else {
+                copy_tile<DV, false>(dst, vc, t0, lo, hi);
+                ++pv;
+            }
+            break;
+        }
+        slot_in = slot_in == kRing - 1 ? 0 : slot_in + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto arrived = [&]() {  // the oldest tile that was asked for
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        __syncwarp();
+        const uint4* t = sm.ring[warp][slot_out];
+        slot_out = slot_out == kRing - 1 ? 0 : slot_out + 1;
+        return t;
+    };
+
     if (s0 < s1) {
+#pragma unroll 1
+        for (int i = 0; i < kRing; ++i) ask();
         // queries: as they are for the tail, and as f16 for the codes, each head's
         // times a power of two that puts its largest near 2^14 (exact)
         for (int i = tid; i < kWarps * DK / 8; i += kDecThreads) {
@@ -393,22 +478,27 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
 
         for (int c0 = s0; c0 < s1; c0 += kChunk) {
             const int c1 = min(c0 + kChunk, s1);
+            // the chunk's scales, a block a lane (32 of 16 slots at most); log2 for the values'
+            const int blk = (c0 >> rs) + lane;
+            const float ksl = blk < nb ? c.k_scale[(size_t)b * nb + blk] : 1.0f;
+            const float vsl = blk < nb ? __log2f(vsc[blk]) : 0.0f;
             // ---- scores
             for (int t0 = c0 + 16 * warp; t0 < c1; t0 += 16 * kWarps) {
-                const int lo = (t0 & ~(R - 1)) == at ? max(t0, cur + 1) : t0, hi = min(t0 + 16, n);
-                if (lo >= hi) continue;  // all of them in the tail
-                const float ks = c.k_scale[(size_t)b * nb + (t0 >> rs)];
+                int lo, hi;
+                bounds(t0, c1, lo, hi);
+                const float ks = __shfl_sync(0xffffffffu, ksl, (t0 - c0) >> rs);
+                const uint4* tile = arrived();
                 uint32_t ka[2][KW];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {  // rows without a token of the cache repeat one that has
-                    const int u = min(max(t0 + g + 8 * r, lo), hi - 1);
-                    const uint4* row = reinterpret_cast<const uint4*>(kc + (size_t)u * DK);
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int x = 0; x < DK / 64; ++x) {
-                        const uint4 v = row[4 * x + l4];
+                        const uint4 v = tile[tile_place<DK, true>(g + 8 * r, 4 * x + l4)];
                         ka[r][4 * x] = v.x; ka[r][4 * x + 1] = v.y; ka[r][4 * x + 2] = v.z; ka[r][4 * x + 3] = v.w;
                     }
-                }
+                __syncwarp();
+                ask();
+                if (lo >= hi) continue;  // all of them in the tail
                 float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
@@ -454,11 +544,15 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
             // ---- weights of this warp's head, and its values
             if (busy) {
                 float cm = -INFINITY, cm2 = -3e38f;
-                for (int u = c0 + lane; u < c1; u += 32) {
-                    const float s = sc[hd][u - c0];
-                    const bool tl = u >= at && u <= cur;
-                    cm = fmaxf(cm, s);
-                    cm2 = fmaxf(cm2, tl ? s : s + __log2f(vsc[u >> rs]));
+#pragma unroll 4
+                for (int u0 = c0; u0 < c1; u0 += 32) {
+                    const int u = u0 + lane;
+                    const float ls = __shfl_sync(0xffffffffu, vsl, (u - c0) >> rs & 31);
+                    if (u < c1) {
+                        const float s = sc[hd][u - c0];
+                        cm = fmaxf(cm, s);
+                        cm2 = fmaxf(cm2, u >= at && u <= cur ? s : s + ls);
+                    }
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) {
@@ -475,38 +569,46 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[i][e] *= f2;
                 const int tiles = (c1 - c0 + 15) / 16;
-                for (int i = lane; i < ((tiles - sub + wph - 1) / wph) * 16; i += 32) {
-                    const int x = 16 * (sub + wph * (i >> 4)) + (i & 15), u = c0 + x;
+                const int mine = ((tiles - sub + wph - 1) / wph) * 16;
+#pragma unroll 4
+                for (int i0 = 0; i0 < mine; i0 += 32) {
+                    const int i = i0 + lane, x = 16 * (sub + wph * (i >> 4)) + (i & 15), u = c0 + x;
+                    const float ls = __shfl_sync(0xffffffffu, vsl, x >> rs & 31);
                     float e = 0.0f;
-                    if (u < c1) {
+                    if (i < mine && u < c1) {
                         const float s = sc[hd][x];
                         l += ex2_fast(s - m);
-                        if (u < at || u > cur) e = ex2_fast(s + __log2f(vsc[u >> rs]) - m2);
+                        if (u < at || u > cur) e = ex2_fast(s + ls - m2);
                     }
-                    const __half hi = __float2half_rn(e);
-                    wt[warp][0][i] = hi;
-                    wt[warp][1][i] = __float2half_rn(e - __half2float(hi));
+                    if (i < mine) {
+                        const __half hi = __float2half_rn(e);
+                        wt[warp][0][i] = hi;
+                        wt[warp][1][i] = __float2half_rn(e - __half2float(hi));
+                    }
                 }
                 __syncwarp();
                 int k = 0;
-#pragma unroll 2
+#pragma unroll 1
                 for (int tt = sub; tt < tiles; tt += wph, ++k) {
                     const int t0 = c0 + 16 * tt;
-                    const int lo = (t0 & ~(R - 1)) == at ? max(t0, cur + 1) : t0, hi = min(t0 + 16, c1);
-                    if (lo >= hi) continue;
+                    int lo, hi;
+                    bounds(t0, c1, lo, hi);
+                    const uint4* tile = arrived();
                     uint32_t v[4][VB / 4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {  // tokens 2 l4, 2 l4 + 1, and 8 on
-                        const int u = min(max(t0 + 2 * l4 + (r & 1) + 4 * (r & 2), lo), hi - 1);
-                        const unsigned char* row = vc + (size_t)u * DV + VB * g;
+                        const int row = 2 * l4 + (r & 1) + 4 * (r & 2);
                         if (VB == 16) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(row);
+                            const uint4 x = tile[tile_place<DV, false>(row, g)];
                             v[r][0] = x.x; v[r][1] = x.y; v[r][VB / 4 - 2] = x.z; v[r][VB / 4 - 1] = x.w;
                         } else {
-                            const uint2 x = *reinterpret_cast<const uint2*>(row);
+                            const uint2 x = reinterpret_cast<const uint2*>(tile + tile_place<DV, false>(row, g >> 1))[g & 1];
                             v[r][0] = x.x; v[r][1] = x.y;
                         }
                     }
+                    __syncwarp();
+                    ask();
+                    if (lo >= hi) continue;
                     uint32_t b0 = 0, b1 = 0;
                     if (g < 2) {
                         b0 = *reinterpret_cast<const uint32_t*>(&wt[warp][g][16 * k + 2 * l4]);
@@ -612,32 +714,52 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
     }
 }
 
-// Joins the splits of a window, one warp a head, and advances the positions.
+// Joins the splits of a window, one CTA a head, and advances the positions.
+constexpr int kJoinThreads = 256, kMostSplits = 128;
 template <int DV>
-__global__ void __launch_bounds__(128) ska_q8_join_kernel(const SkaQ8DecodeParams p, const Q8Plan pl) {
+__global__ void __launch_bounds__(kJoinThreads) ska_q8_join_kernel(const SkaQ8DecodeParams p, const Q8Plan pl) {
+    constexpr int ROWS = kJoinThreads / DV;
+    __shared__ float f[kMostSplits], red[2][kJoinThreads / 32], part[ROWS][DV];
     const SkaQ8Cache& c = p.c;
-    const int bh = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (bh >= c.B * c.H) return;
-    const int b = bh / c.H, pos = c.pos[b];
+    const int bh = blockIdx.x, tid = threadIdx.x, b = bh / c.H, pos = c.pos[b];
     if (pos < 0) return;
-    const float* m = pl.m + (size_t)bh * pl.splits;
-    const float* l = pl.l + (size_t)bh * pl.splits;
-    float mx = -INFINITY;
-    for (int k = 0; k < pl.splits; ++k) mx = fmaxf(mx, m[k]);
-    float sum = 0.0f, a[DV / 32] = {};
-    for (int k = 0; k < pl.splits; ++k) {
-        if (m[k] == -INFINITY) continue;
-        const float f = ex2_fast(m[k] - mx);
-        sum = fmaf(f, l[k], sum);
+    // a split's share is 2^(m_k - m); one without slots has m_k = -inf and no values
+    float m = tid < pl.splits ? pl.m[(size_t)bh * pl.splits + tid] : -INFINITY;
+    const float l = tid < pl.splits ? pl.l[(size_t)bh * pl.splits + tid] : 0.0f;
+    float mx = m;
 #pragma unroll
-        for (int i = 0; i < DV / 32; ++i)
-            a[i] = fmaf(f, pl.o[((size_t)bh * pl.splits + k) * DV + 32 * i + lane], a[i]);
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if ((tid & 31) == 0) red[0][tid >> 5] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kJoinThreads / 32; ++k) mx = fmaxf(mx, red[0][k]);
+    const float share = m == -INFINITY ? 0.0f : ex2_fast(m - mx);
+    if (tid < pl.splits) f[tid] = share;
+    float sum = share * l;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((tid & 31) == 0) red[1][tid >> 5] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoinThreads / 32; ++k) sum += red[1][k];
+    const int x = tid % DV, row = tid / DV;
+    const float* o = pl.o + (size_t)bh * pl.splits * DV + x;
+    float a = 0.0f;
+#pragma unroll 8
+    for (int k = row; k < pl.splits; k += ROWS) {
+        const float v = o[(size_t)k * DV];
+        a = f[k] == 0.0f ? a : fmaf(f[k], v, a);
     }
+    part[row][x] = a;
+    __syncthreads();
+    if (tid < DV) {
 #pragma unroll
-    for (int i = 0; i < DV / 32; ++i)
-        static_cast<__nv_bfloat16*>(p.o)[(size_t)bh * DV + 32 * i + lane] = __float2bfloat16_rn(a[i] / sum);
-    // a sequence's other warps only ask whether pos is negative
-    if (p.advance && bh % c.H == 0 && lane == 0) c.pos[b] = pos + 1;
+        for (int k = 1; k < ROWS; ++k) a += part[k][x];
+        static_cast<__nv_bfloat16*>(p.o)[(size_t)bh * DV + x] = __float2bfloat16_rn(a / sum);
+    }
+    // a sequence's other CTAs only ask whether pos is negative
+    if (p.advance && bh % c.H == 0 && tid == 0) c.pos[b] = pos + 1;
 }
 
 __global__ void ska_q8_advance_kernel(int* pos, int B) {
@@ -669,7 +791,7 @@ Q8Plan plan(const SkaQ8DecodeParams& p) {
     const long long units = (long long)p.c.B * pl.groups;
     // two CTAs an SM; each split of at least 256 slots, in multiples of the largest block
     long long P = units > 0 ? 2LL * sm_count() / units : 1;
-    const long long most = (p.c.window + 255) / 256;
+    const long long most = (p.c.window + 255) / 256;  // at most kMostSplits, the window at most 32768
     if (P > most) P = most;
     if (P < 1) P = 1;
     const int range = (int)((p.c.window + P - 1) / P + 63) / 64 * 64;
@@ -701,6 +823,7 @@ cudaError_t launch_decode_cfg(const SkaQ8DecodeParams& p, Q8Plan pl, cudaStream_
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)p.c.B * pl.groups), pl.splits);
     cfg.blockDim = dim3(kDecThreads);
+    cfg.dynamicSmemBytes = sizeof(Q8Smem<DK, DV>);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     if (pl.cluster) {
@@ -711,10 +834,12 @@ cudaError_t launch_decode_cfg(const SkaQ8DecodeParams& p, Q8Plan pl, cudaStream_
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    cudaError_t e = cudaLaunchKernelEx(&cfg, ska_q8_decode_kernel<I8, DK, DV>, p, pl);
+    auto kern = ska_q8_decode_kernel<I8, DK, DV>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, p, pl);
     if (e != cudaSuccess) return e;
     if (pl.splits > 1) {
-        ska_q8_join_kernel<DV><<<(unsigned)(((long long)p.c.B * p.c.H + 3) / 4), 128, 0, s>>>(p, pl);
+        ska_q8_join_kernel<DV><<<(unsigned)(p.c.B * p.c.H), kJoinThreads, 0, s>>>(p, pl);
         e = cudaGetLastError();
     } else if (!pl.cluster && p.advance) {
         ska_q8_advance_kernel<<<(p.c.B + 255) / 256, 256, 0, s>>>(p.c.pos, p.c.B);
