@@ -279,6 +279,7 @@ struct Q8Smem {
     __nv_bfloat16 qs[kWarps][DK];
     float part[kWarps][DV];
     float stat[kWarps][3];
+    __half zero[16];
 };
 
 // Place of 16-byte piece x of row r in a tile of 16 rows, such that the lanes that
@@ -290,29 +291,54 @@ __device__ __forceinline__ int tile_place(int r, int x) {
     const int line = r >> 1, at = (r & 1) * 4 + x;
     return line * 8 + (KEYS ? at : at ^ ((line & 3) << 1));
 }
-
-// Starts the copy of rows t0 .. t0 + 15, those outside [lo, hi) as the nearest inside.
+__device__ __forceinline__ void copy_piece(uint32_t dst, const unsigned char* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Starts the copy of a tile of 16 rows at `src`, which is contiguous.  Lane's
+// pieces are 32 apart, and so are their places, up to one bit for every second.
 template <int D, bool KEYS>
-__device__ __forceinline__ void copy_tile(uint4* dst, const unsigned char* base, int t0, int lo, int hi) {
+__device__ __forceinline__ void copy_tile(uint32_t dst, const unsigned char* src) {
     const int lane = threadIdx.x & 31;
+    const int place = tile_place<D, KEYS>(lane / (D / 16), lane % (D / 16));
+    const uint32_t at = dst + 16 * place, odd = D == 128 && !KEYS ? dst + 16 * (place ^ 4) : at;
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-        const int i = lane + 32 * j, r = i / (D / 16), x = i % (D / 16);
+    for (int j = 0; j < D / 32; ++j) copy_piece((j & 1 ? odd : at) + 512 * j, src + 16 * lane + 512 * j);
+}
+// The same for a tile of which only rows [lo, hi) are in the cache: the others as
+// the nearest that is.
+template <int D, bool KEYS>
+__device__ __noinline__ void copy_edge(uint32_t dst, const unsigned char* base, int t0, int lo, int hi) {
+    const int lane = threadIdx.x & 31;
+    for (int i = lane; i < D; i += 32) {
+        const int r = i / (D / 16), x = i % (D / 16);
         const int u = min(max(t0 + r, lo), hi - 1);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                         (unsigned)__cvta_generic_to_shared(dst + tile_place<D, KEYS>(r, x))),
-                     "l"(base + (size_t)u * D + 16 * x)
-                     : "memory");
+        copy_piece(dst + 16 * tile_place<D, KEYS>(r, x), base + (size_t)u * D + 16 * x);
     }
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -393,44 +419,49 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
         for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
 
     // This warp's tiles in the order in which it takes them: of each chunk first the
-    // keys' (16 slots each, every eighth tile), then the values'.
-    int pc = s0, pk = 0, pv = 0, slot_in = 0, slot_out = 0;  // the next to ask for, ring places
-    auto bounds = [&](int t0, int end, int& lo, int& hi) {  // slots of a tile that are in the cache
+    // keys' (every eighth tile), then the values' (every wph-th).  An edge tile holds
+    // slots of the block being written or behind the last token.
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp][0]);
+    constexpr uint32_t TILE = sizeof(sm.ring[0][0]);
+    int pc = s0, pk = s0 + 16 * warp, pv = s0 + 16 * sub;  // the next to ask for
+    uint32_t slot_in = ring, slot_out = ring;
+    auto is_edge = [&](int t0) { return (t0 & ~(R - 1)) == at || t0 + 16 > s1; };
+    auto bounds = [&](int t0, int& lo, int& hi) {  // slots of a tile that are in the cache
         lo = (t0 & ~(R - 1)) == at ? max(t0, cur + 1) : t0;
-        hi = min(t0 + 16, end);
+        hi = min(t0 + 16, s1);
     };
     auto ask = [&]() {
-        while (pc < s1) {
-            const int c1 = min(pc + kChunk, s1);
-            int t0 = pc + 16 * (warp + kWarps * pk);
-            const bool key = t0 < c1;
-            if (!key) t0 = pc + 16 * (sub + wph * pv);
-            if (!key && (!busy || t0 >= c1)) {
-                pc += kChunk;
-                pk = pv = 0;
-                continue;
-            }
-            int lo, hi;
-            bounds(t0, c1, lo, hi);
-            if (lo >= hi) lo = t0, hi = c1;  // none of them: copied and not used
-            uint4* dst = sm.ring[warp][slot_in];
-            if (key) {
-                copy_tile<DK, true>(dst, kc, t0, lo, hi);
-                ++pk;
+        const int c1 = min(pc + kChunk, s1);
+        if (pk < c1 || (busy && pv < c1)) {
+            const bool key = pk < c1;
+            const int t0 = key ? pk : pv;
+            if (is_edge(t0)) {
+                int lo, hi;
+                bounds(t0, lo, hi);
+                if (lo >= hi) lo = t0, hi = s1;  // none of them: copied and not used
+                if (key) copy_edge<DK, true>(slot_in, kc, t0, lo, hi);
+                else copy_edge<DV, false>(slot_in, vc, t0, lo, hi);
+            } else if (key) {
+                copy_tile<DK, true>(slot_in, kc + (size_t)t0 * DK);
             } else {
-                copy_tile<DV, false>(dst, vc, t0, lo, hi);
-                ++pv;
+                copy_tile<DV, false>(slot_in, vc + (size_t)t0 * DV);
             }
-            break;
+            if (key) pk += 16 * kWarps;
+            else pv += 16 * wph;
+            slot_in = slot_in == ring + (kRing - 1) * TILE ? ring : slot_in + TILE;
+            if (pk >= c1 && (!busy || pv >= c1)) {  // on to the next chunk
+                pc += kChunk;
+                pk = pc + 16 * warp;
+                pv = pc + 16 * sub;
+            }
         }
-        slot_in = slot_in == kRing - 1 ? 0 : slot_in + 1;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto arrived = [&]() {  // the oldest tile that was asked for
         asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
         __syncwarp();
-        const uint4* t = sm.ring[warp][slot_out];
-        slot_out = slot_out == kRing - 1 ? 0 : slot_out + 1;
+        const uint32_t t = slot_out;
+        slot_out = slot_out == ring + (kRing - 1) * TILE ? ring : slot_out + TILE;
         return t;
     };
 
@@ -445,6 +476,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
             if (hh < nh) v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (bh0 + hh) * DK)[x];
             reinterpret_cast<uint4*>(qs[hh])[x] = v;
         }
+        if (tid < 16) sm.zero[tid] = __half(0.0f);
         __syncthreads();
         // lane's dimensions of a row: 16 l4 .. + 15, and 64 more on for d_k = 128; heads by g
         uint32_t qf[KW][2];
@@ -485,15 +517,15 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
             // ---- scores
             for (int t0 = c0 + 16 * warp; t0 < c1; t0 += 16 * kWarps) {
                 int lo, hi;
-                bounds(t0, c1, lo, hi);
+                bounds(t0, lo, hi);
                 const float ks = __shfl_sync(0xffffffffu, ksl, (t0 - c0) >> rs);
-                const uint4* tile = arrived();
+                const uint32_t tile = arrived();
                 uint32_t ka[2][KW];
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int x = 0; x < DK / 64; ++x) {
-                        const uint4 v = tile[tile_place<DK, true>(g + 8 * r, 4 * x + l4)];
+                        const uint4 v = lds128(tile + 16 * tile_place<DK, true>(g + 8 * r, 4 * x + l4));
                         ka[r][4 * x] = v.x; ka[r][4 * x + 1] = v.y; ka[r][4 * x + 2] = v.z; ka[r][4 * x + 3] = v.w;
                     }
                 __syncwarp();
@@ -587,32 +619,36 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
                     }
                 }
                 __syncwarp();
-                int k = 0;
-#pragma unroll 1
-                for (int tt = sub; tt < tiles; tt += wph, ++k) {
-                    const int t0 = c0 + 16 * tt;
-                    int lo, hi;
-                    bounds(t0, c1, lo, hi);
-                    const uint4* tile = arrived();
+                // lanes g = 0 and 1 have the weights' halves, the others zeros
+                uint32_t wp = (uint32_t)__cvta_generic_to_shared(g < 2 ? &wt[warp][g][2 * l4] : &sm.zero[2 * l4]);
+                const uint32_t wstep = g < 2 ? 32 : 0;
+                // rows 2 l4 and 2 l4 + 1; 8 on lies 8 rows further
+                const uint32_t off0 = VB == 16 ? 16 * tile_place<DV, false>(2 * l4, g)
+                                               : 16 * tile_place<DV, false>(2 * l4, g >> 1) + 8 * (g & 1);
+                const uint32_t off1 = VB == 16 ? 16 * tile_place<DV, false>(2 * l4 + 1, g)
+                                               : 16 * tile_place<DV, false>(2 * l4 + 1, g >> 1) + 8 * (g & 1);
+#pragma unroll 2
+                for (int t0 = c0 + 16 * sub; t0 < c1; t0 += 16 * wph, wp += wstep) {
+                    const uint32_t tile = arrived();
                     uint32_t v[4][VB / 4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {  // tokens 2 l4, 2 l4 + 1, and 8 on
-                        const int row = 2 * l4 + (r & 1) + 4 * (r & 2);
+                        const uint32_t a = tile + (r & 1 ? off1 : off0) + (r & 2 ? 8 * DV : 0);
                         if (VB == 16) {
-                            const uint4 x = tile[tile_place<DV, false>(row, g)];
+                            const uint4 x = lds128(a);
                             v[r][0] = x.x; v[r][1] = x.y; v[r][VB / 4 - 2] = x.z; v[r][VB / 4 - 1] = x.w;
                         } else {
-                            const uint2 x = reinterpret_cast<const uint2*>(tile + tile_place<DV, false>(row, g >> 1))[g & 1];
+                            const uint2 x = lds64(a);
                             v[r][0] = x.x; v[r][1] = x.y;
                         }
                     }
+                    const uint32_t b0 = lds32(wp), b1 = lds32(wp + 16);
                     __syncwarp();
                     ask();
-                    if (lo >= hi) continue;
-                    uint32_t b0 = 0, b1 = 0;
-                    if (g < 2) {
-                        b0 = *reinterpret_cast<const uint32_t*>(&wt[warp][g][16 * k + 2 * l4]);
-                        b1 = *reinterpret_cast<const uint32_t*>(&wt[warp][g][16 * k + 2 * l4 + 8]);
+                    if (is_edge(t0)) {
+                        int lo, hi;
+                        bounds(t0, lo, hi);
+                        if (lo >= hi) continue;  // all of them in the tail
                     }
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {  // columns VB g + 2 i and + 1
