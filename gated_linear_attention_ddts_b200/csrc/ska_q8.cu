@@ -276,9 +276,11 @@ struct Q8Smem {
     uint4 ring[kWarps][kRing][16 * (DK > DV ? DK : DV) / 16];
     float sc[kWarps][kStride];
     __half wt[kWarps][2][kChunk];
-    __nv_bfloat16 qs[kWarps][DK];
+    __nv_bfloat16 qs[kWarps][DK + 8];  // rows 16 bytes off one another's banks
     float part[kWarps][DV];
     float stat[kWarps][3];
+    float lvs[kWarps][32];             // log2 of the chunk's value scales, by head and block
+    float mx[kWarps][kWarps][2];       // a warp's largest scores by head, without and with the scales
     __half zero[16];
 };
 
@@ -348,6 +350,8 @@ __device__ __forceinline__ float finite_abs(float x) {
     return a <= 3.4e38f ? a : 0.0f;  // neither infinite nor NaN (bf16 ends at 3.39e38)
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Four codes as two f16 pairs.
 template <bool I8>
 __device__ __forceinline__ uint2 f16_pairs(uint32_t w) {
@@ -410,7 +414,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
     const int wph = kWarps / nh, hd = min(warp / wph, nh - 1), sub = warp % wph;
     const bool busy = warp < wph * nh;
     const unsigned char* vc = c.v + (bh0 + hd) * w * DV;
-    const float* vsc = c.v_scale + (bh0 + hd) * nb;
     float m = -INFINITY, m2 = -3e38f, l = 0.0f;  // m of the scores, m2 with the scales in them
     float acc[MT][4];
 #pragma unroll
@@ -468,6 +471,22 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
     if (s0 < s1) {
 #pragma unroll 1
         for (int i = 0; i < kRing; ++i) ask();
+        // the new token's row of the tail (read from the inputs below), and the rows
+        // before it toward L2
+        if (tail_here) {
+            if (group == 0 && tid < DK / 8)
+                reinterpret_cast<uint4*>(kt + (size_t)fill * DK)[tid] = reinterpret_cast<const uint4*>(kin)[tid];
+            for (int i = tid; i < nh * (DV / 8); i += kDecThreads) {
+                const int hh = i / (DV / 8), x = i % (DV / 8);
+                reinterpret_cast<uint4*>(vt + ((size_t)hh * R + fill) * DV)[x] =
+                    reinterpret_cast<const uint4*>(vin + (size_t)hh * DV)[x];
+            }
+            for (int i = tid; i < fill * DK / 64; i += kDecThreads) prefetch_l2(kt + 64 * i);
+            for (int i = tid; i < nh * fill * DV / 64; i += kDecThreads) {
+                const int hh = i / (fill * DV / 64), x = i % (fill * DV / 64);
+                prefetch_l2(vt + (size_t)hh * R * DV + 64 * x);
+            }
+        }
         // queries: as they are for the tail, and as f16 for the codes, each head's
         // times a power of two that puts its largest near 2^14 (exact)
         for (int i = tid; i < kWarps * DK / 8; i += kDecThreads) {
@@ -482,12 +501,16 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
         uint32_t qf[KW][2];
         float qmul;
         {
-            float most = 0.0f;
+            float qv[KW][4], most = 0.0f;
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
-                const int d = (j >> 2) * 64 + l4 * 16 + (j & 3) * 4;
+                const uint2 u = *reinterpret_cast<const uint2*>(&qs[g][(j >> 2) * 64 + l4 * 16 + (j & 3) * 4]);
+                qv[j][0] = __uint_as_float(u.x << 16);
+                qv[j][1] = __uint_as_float(u.x & 0xffff0000u);
+                qv[j][2] = __uint_as_float(u.y << 16);
+                qv[j][3] = __uint_as_float(u.y & 0xffff0000u);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) most = fmaxf(most, finite_abs(__bfloat162float(qs[g][d + e])));
+                for (int e = 0; e < 4; ++e) most = fmaxf(most, finite_abs(qv[j][e]));
             }
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
@@ -496,14 +519,12 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
             const float inv = __uint_as_float((unsigned)(127 - e2) << 23);
             qmul = __uint_as_float((unsigned)(127 + e2) << 23) * (p.scale * kLog2e);
 #pragma unroll
-            for (int j = 0; j < KW; ++j) {
-                const int d = (j >> 2) * 64 + l4 * 16 + (j & 3) * 4;
+            for (int j = 0; j < KW; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    __half2 hv = __floats2half2_rn(__bfloat162float(qs[g][d + 2 * e]) * inv, __bfloat162float(qs[g][d + 2 * e + 1]) * inv);
-                    qf[j][e] = *reinterpret_cast<uint32_t*>(&hv);
+                    const __half2 hv = __floats2half2_rn(qv[j][2 * e] * inv, qv[j][2 * e + 1] * inv);
+                    qf[j][e] = *reinterpret_cast<const uint32_t*>(&hv);
                 }
-            }
         }
         // multipliers of the two heads whose scores this lane gets from an mma
         const float qm0 = __shfl_sync(0xffffffffu, qmul, 8 * l4), qm1 = __shfl_sync(0xffffffffu, qmul, 8 * l4 + 4);
@@ -513,7 +534,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
             // the chunk's scales, a block a lane (32 of 16 slots at most); log2 for the values'
             const int blk = (c0 >> rs) + lane;
             const float ksl = blk < nb ? c.k_scale[(size_t)b * nb + blk] : 1.0f;
-            const float vsl = blk < nb ? __log2f(vsc[blk]) : 0.0f;
+            if (warp < nh) sm.lvs[warp][lane] = blk < nb ? __log2f(c.v_scale[(bh0 + warp) * nb + blk]) : 0.0f;
+            __syncthreads();
+            float cm[2] = {-INFINITY, -INFINITY}, cn[2] = {-3e38f, -3e38f};  // of heads 2 l4 and 2 l4 + 1
             // ---- scores
             for (int t0 = c0 + 16 * warp; t0 < c1; t0 += 16 * kWarps) {
                 int lo, hi;
@@ -542,8 +565,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
                 for (int r = 0; r < 2; ++r) {
                     const int u = t0 + g + 8 * r;
                     if (u < lo || u >= hi) continue;
-                    sc[2 * l4][u - c0] = s[2 * r] * (ks * qm0);
-                    sc[2 * l4 + 1][u - c0] = s[2 * r + 1] * (ks * qm1);
+                    const float a = s[2 * r] * (ks * qm0), e = s[2 * r + 1] * (ks * qm1);
+                    sc[2 * l4][u - c0] = a;
+                    sc[2 * l4 + 1][u - c0] = e;
+                    cm[0] = fmaxf(cm[0], a);
+                    cm[1] = fmaxf(cm[1], e);
+                    cn[0] = fmaxf(cn[0], a + sm.lvs[2 * l4][(t0 - c0) >> rs]);
+                    cn[1] = fmaxf(cn[1], e + sm.lvs[2 * l4 + 1][(t0 - c0) >> rs]);
                 }
             }
             const bool tail_now = tail_here && at >= c0 && at < c0 + kChunk;
@@ -568,30 +596,36 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
                     for (int r = 0; r < 2; ++r) {
                         const int i = t0 + g + 8 * r;
                         if (i > fill) continue;
-                        sc[2 * l4][at - c0 + i] = s[2 * r] * (p.scale * kLog2e);
-                        sc[2 * l4 + 1][at - c0 + i] = s[2 * r + 1] * (p.scale * kLog2e);
-                    }
-                }
-            __syncthreads();
-            // ---- weights of this warp's head, and its values
-            if (busy) {
-                float cm = -INFINITY, cm2 = -3e38f;
-#pragma unroll 4
-                for (int u0 = c0; u0 < c1; u0 += 32) {
-                    const int u = u0 + lane;
-                    const float ls = __shfl_sync(0xffffffffu, vsl, (u - c0) >> rs & 31);
-                    if (u < c1) {
-                        const float s = sc[hd][u - c0];
-                        cm = fmaxf(cm, s);
-                        cm2 = fmaxf(cm2, u >= at && u <= cur ? s : s + ls);
+                        const float a = s[2 * r] * (p.scale * kLog2e), e = s[2 * r + 1] * (p.scale * kLog2e);
+                        sc[2 * l4][at - c0 + i] = a;
+                        sc[2 * l4 + 1][at - c0 + i] = e;
+                        cm[0] = fmaxf(cm[0], a);
+                        cm[1] = fmaxf(cm[1], e);
+                        cn[0] = fmaxf(cn[0], a);
+                        cn[1] = fmaxf(cn[1], e);
                     }
                 }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
-                    cm2 = fmaxf(cm2, __shfl_xor_sync(0xffffffffu, cm2, o));
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    cm[k] = fmaxf(cm[k], __shfl_xor_sync(0xffffffffu, cm[k], o));
+                    cn[k] = fmaxf(cn[k], __shfl_xor_sync(0xffffffffu, cn[k], o));
                 }
-                const float nm = fmaxf(m, cm), nm2 = fmaxf(m2, cm2);
+                if (g == 0) {
+                    sm.mx[warp][2 * l4 + k][0] = cm[k];
+                    sm.mx[warp][2 * l4 + k][1] = cn[k];
+                }
+            }
+            __syncthreads();
+            // ---- weights of this warp's head, and its values
+            if (busy) {
+                float nm = m, nm2 = m2;
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) {
+                    nm = fmaxf(nm, sm.mx[k][hd][0]);
+                    nm2 = fmaxf(nm2, sm.mx[k][hd][1]);
+                }
                 const float f2 = ex2_fast(m2 - nm2);
                 l *= m == nm ? 1.0f : ex2_fast(m - nm);
                 m = nm;
@@ -602,21 +636,25 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
                     for (int e = 0; e < 4; ++e) acc[i][e] *= f2;
                 const int tiles = (c1 - c0 + 15) / 16;
                 const int mine = ((tiles - sub + wph - 1) / wph) * 16;
-#pragma unroll 4
-                for (int i0 = 0; i0 < mine; i0 += 32) {
-                    const int i = i0 + lane, x = 16 * (sub + wph * (i >> 4)) + (i & 15), u = c0 + x;
-                    const float ls = __shfl_sync(0xffffffffu, vsl, x >> rs & 31);
-                    float e = 0.0f;
-                    if (i < mine && u < c1) {
-                        const float s = sc[hd][x];
-                        l += ex2_fast(s - m);
-                        if (u < at || u > cur) e = ex2_fast(s + ls - m2);
+                for (int i = 4 * lane; i < mine; i += 128) {  // four neighbouring slots a lane
+                    const int x = 16 * (sub + wph * (i >> 4)) + (i & 15), u = c0 + x;
+                    const float ls = sm.lvs[hd][x >> rs] - m2;
+                    const float4 s4 = *reinterpret_cast<const float4*>(&sc[hd][x]);
+                    const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+                    float e[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const bool in = u + k < c1;
+                        l += in ? ex2_fast(sv[k] - m) : 0.0f;
+                        e[k] = in && (u + k < at || u + k > cur) ? ex2_fast(sv[k] + ls) : 0.0f;
                     }
-                    if (i < mine) {
-                        const __half hi = __float2half_rn(e);
-                        wt[warp][0][i] = hi;
-                        wt[warp][1][i] = __float2half_rn(e - __half2float(hi));
-                    }
+                    const __half2 h0 = __floats2half2_rn(e[0], e[1]), h1 = __floats2half2_rn(e[2], e[3]);
+                    const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+                    const __half2 r0 = __floats2half2_rn(e[0] - f0.x, e[1] - f0.y), r1 = __floats2half2_rn(e[2] - f1.x, e[3] - f1.y);
+                    *reinterpret_cast<uint2*>(&wt[warp][0][i]) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+                    *reinterpret_cast<uint2*>(&wt[warp][1][i]) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&r0), *reinterpret_cast<const uint32_t*>(&r1));
                 }
                 __syncwarp();
                 // lanes g = 0 and 1 have the weights' halves, the others zeros
@@ -673,13 +711,19 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
                         }
                         const uint32_t b0 = bf16_pair(e[0], e[1]), b1 = bf16_pair(e[2], e[3]);
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            uint32_t v[4];
+                        for (int x = 0; x < VB / 8; ++x) {  // eight columns of the four rows at once
+                            uint32_t v[4][4];
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) v[r] = *reinterpret_cast<const uint32_t*>(row[r] + 2 * i);
-                            const uint32_t a[4] = {__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632),
-                                                   __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[2], v[3], 0x7632)};
-                            mma_bf16(acc[i], a, b0, b1);
+                            for (int r = 0; r < 4; ++r) {
+                                const uint4 q = *reinterpret_cast<const uint4*>(row[r] + 8 * x);
+                                v[r][0] = q.x; v[r][1] = q.y; v[r][2] = q.z; v[r][3] = q.w;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t a[4] = {__byte_perm(v[0][i], v[1][i], 0x5410), __byte_perm(v[0][i], v[1][i], 0x7632),
+                                                       __byte_perm(v[2][i], v[3][i], 0x5410), __byte_perm(v[2][i], v[3][i], 0x7632)};
+                                mma_bf16(acc[4 * x + i], a, b0, b1);
+                            }
                         }
                     }
             }
@@ -727,14 +771,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
                 }
             }
         }
-    // ---- the new token, and the block if it is full with it
+    // ---- the block if it is full with the new token
     if (tail_here) {
-        if (group == 0 && tid < DK / 8)
-            reinterpret_cast<uint4*>(kt + (size_t)fill * DK)[tid] = reinterpret_cast<const uint4*>(kin)[tid];
-        for (int i = tid; i < nh * (DV / 8); i += kDecThreads) {
-            const int hh = i / (DV / 8), x = i % (DV / 8);
-            reinterpret_cast<uint4*>(vt + ((size_t)hh * R + fill) * DV)[x] = reinterpret_cast<const uint4*>(vin + (size_t)hh * DV)[x];
-        }
         if (cur == w - 1 || fill == R - 1) {
             __syncthreads();
             if (group == 0)
