@@ -40,14 +40,6 @@ struct SegArgs {
     float *local, *dsum;
 };
 
-// 16 bytes from global into shared memory without passing registers; zeros where
-// `there` is false.
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(there ? 16 : 0)
-                 : "memory");
-}
-
 // Threads of the element-wise warps: one for each two channels by four tokens of
 // a tile.
 template <int CPB>

@@ -44,188 +44,490 @@ struct Red {
     static constexpr int F = N <= 32 ? 16 : N == 64 ? 8 : 2;  // tokens between two sums over the warps
 };
 
-// A chunk's delta, u, p of the block's channels into shared memory, and the
-// factors that the last stage needs; tokens at or behind `end` count as zeros.
+// Threads of the element-wise warps: one for each two channels by four tokens of
+// a chunk.
+template <int CPB>
+constexpr int kEw = kQuads * (CPB / 2) < 32 ? 32 : kQuads * (CPB / 2);
+
 template <typename T, int N, int CPB, bool LOCAL>
-__global__ void __launch_bounds__(CPB * N / 4) ssm_bwd_kernel(const SsmBwdParams bp, const BwdWork wk) {
+struct BwdSmem {
     using L = Lay<N, CPB>;
-    constexpr int LPC = L::LPC, TH = L::THREADS, UNITS = kQuads * (CPB / 2), WARPS = TH / 32, F = Red<N>::F;
+    using Arr = float[kQuads][L::PLACES][4];
+    static constexpr int M = LOCAL ? 1 : 2;
+    Arr D[2], P[2];              // delta, p
+    Arr U[M];
+    Arr Y[M], Q[M], E[M];        // sums over n: C s, G B, w A
+    Arr F[M], S[M], Z[M];        // silu'(zc), d delta / d dt, go silu'(z); the element-wise threads' own
+    float C5[M][LOCAL ? 1 : kQuads + 1][L::PLACES][4];  // dzc, and the chunk behind's first four
+    typename Four<T>::Raw B[LOCAL ? 1 : 3][kSsmChunk][N / 4];
+    typename Four<T>::Raw C[3][kSsmChunk][N / 4];
+    float R[LOCAL ? 1 : L::THREADS / 32][LOCAL ? 1 : Red<N>::F][2 * N];
+    float par[kPar][kQuads][CPB];
+};
+
+// The second evaluation of a decay: not to be taken for the first one, whose 64
+// values a thread cannot keep beside the chunk's states.
+__device__ __forceinline__ float2 decay_again(float2 d, float2 a) {
+    float2 r;
+    asm volatile("mul.rn.f32x2 %0, %1, %2;"
+                 : "=l"(reinterpret_cast<uint64_t&>(r)) : "l"(reinterpret_cast<uint64_t&>(d)), "l"(reinterpret_cast<uint64_t&>(a)));
+    return ex22(r);
+}
+template <int ID, int THREADS>
+__device__ __forceinline__ void part_sync() {
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+
+// Scan warps and element-wise warps, a chunk apart as in the forward: while the
+// scan warps run chunk k (forward, then backwards), the others finish chunk k - 1
+// and make delta, u and p of chunk k + 1.
+template <typename T, int N, int CPB, bool LOCAL>
+__global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 : CPB * N / 4 > 64 ? 3 : 4)
+    ssm_bwd_kernel(const SsmBwdParams bp, const BwdWork wk) {
+    using L = Lay<N, CPB>;
+    using Raw = typename Pair<T>::Raw;
+    using Quad = typename Four<T>::Raw;
+    constexpr int LPC = L::LPC, TH = L::THREADS, EW = kEw<CPB>, UNITS = kQuads * (CPB / 2), WARPS = TH / 32, F = Red<N>::F;
     constexpr int CW = 32 / LPC;  // channels a warp
-    static_assert(UNITS <= TH, "one unit a thread");
-    __shared__ __align__(16) float sD[kQuads][L::PLACES][4];
-    __shared__ __align__(16) float sU[kQuads][L::PLACES][4];
-    __shared__ __align__(16) float sP[kQuads][L::PLACES][4];
-    __shared__ __align__(16) float sY[LOCAL ? 1 : kQuads][L::PLACES][4];
-    __shared__ __align__(16) float sQ[LOCAL ? 1 : kQuads][L::PLACES][4];
-    __shared__ __align__(16) float sE[LOCAL ? 1 : kQuads][L::PLACES][4];
-    __shared__ __align__(16) float sF[LOCAL ? 1 : kQuads][L::PLACES][4];      // silu'(zc)
-    __shared__ __align__(16) float sS[LOCAL ? 1 : kQuads][L::PLACES][4];      // d delta / d dt
-    __shared__ __align__(16) float sZ[LOCAL ? 1 : kQuads + 1][L::PLACES][4];  // dzc, and the next chunk's first four
-    __shared__ __align__(16) float sB[LOCAL ? 1 : kSsmChunk][N];
-    __shared__ __align__(16) float sC[kSsmChunk][N];
-    __shared__ __align__(16) float sR[LOCAL ? 1 : WARPS][LOCAL ? 1 : F][2 * N];
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    BwdSmem<T, N, CPB, LOCAL>& sm = *reinterpret_cast<BwdSmem<T, N, CPB, LOCAL>*>(smem_raw);
     const SsmParams& p = bp.f;
     const int bh = blockIdx.x / wk.nblk, blk = blockIdx.x % wk.nblk, c0 = blk * CPB;
     const int b = bh / p.H, h = bh % p.H, seg = blockIdx.y + (LOCAL ? 1 : 0);
     const int len = seq_len(p, b);
     const int begin = seg * wk.len, segend = min(begin + wk.len, p.T);
     const int end = min(segend, len);
-    const int tid = threadIdx.x;
     if (LOCAL && begin >= len) return;
+    const int chunks = end > begin ? (end - begin + kSsmChunk - 1) / kSsmChunk : 0;
+    const int tlast = begin + (chunks - 1) * kSsmChunk;  // first token of the chunk that is taken first
     const size_t row0 = (size_t)bh * p.T;
-    const T* x = static_cast<const T*>(p.x) + row0 * p.D + c0;
-    const T* dt = static_cast<const T*>(p.dt) + row0 * p.D + c0;
-    const T* z = p.z ? static_cast<const T*>(p.z) + row0 * p.D + c0 : nullptr;
-    const T* gy = static_cast<const T*>(bp.gy) + row0 * p.D + c0;
-    const size_t grow = (size_t)(b * p.G + h / (p.H / p.G)) * p.T;
-    const T* Bm = static_cast<const T*>(p.Bm) + grow * N;
-    const T* Cm = static_cast<const T*>(p.Cm) + grow * N;
-    const T* cs = p.cs_in ? static_cast<const T*>(p.cs_in) + (size_t)bh * (p.W - 1) * p.D + c0 : nullptr;
     const size_t states = (size_t)p.B * p.H * p.D;
 
-    const int ch = tid / LPC, sl = tid % LPC, place = L::place(ch);
-    const size_t srow = ((size_t)bh * p.D + c0 + ch) * N + 4 * sl;
-    float A2[4], G[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dA[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dsum = 0.0f;
-    {
-        const float4 a = ld4(p.A + ((size_t)h * p.D + c0 + ch) * N + 4 * sl);
-        A2[0] = a.x * kLog2e; A2[1] = a.y * kLog2e; A2[2] = a.z * kLog2e; A2[3] = a.w * kLog2e;
-    }
-    if (!LOCAL) {
-        if (bp.gST) {
-            const float4 v = ld4(bp.gST + srow);
-            G[0] = v.x; G[1] = v.y; G[2] = v.z; G[3] = v.w;
-        }
-        for (int j = wk.P - 1; j > seg; --j) {  // the segments behind this one
-            if (j * wk.len >= len) continue;
-            const float4 v = *reinterpret_cast<const float4*>(wk.local + j * states * N + srow);
-            const float ds = wk.dsum[j * states + (size_t)bh * p.D + c0 + ch];
-            G[0] = fmaf(ex2_fast(A2[0] * ds), G[0], v.x);
-            G[1] = fmaf(ex2_fast(A2[1] * ds), G[1], v.y);
-            G[2] = fmaf(ex2_fast(A2[2] * ds), G[2], v.z);
-            G[3] = fmaf(ex2_fast(A2[3] * ds), G[3], v.w);
-        }
-    }
-    // the element-wise stages: channels cp, cp + 1 of tokens 4 uq .. 4 uq + 3 of the chunk
-    const bool has_unit = tid < UNITS;
-    const int uq = tid / (CPB / 2), cp = 2 * (tid % (CPB / 2)), pl = cp >> 1;
-    float w[4][2] = {}, cb[2] = {0.0f, 0.0f}, bias[2] = {0.0f, 0.0f}, feed[2] = {0.0f, 0.0f};
-    float par[kPar][2] = {};
-    if (has_unit) {
+    if (threadIdx.x >= TH) {  // ---------------- element-wise warps
+        const int tid = threadIdx.x - TH;
+        const T* x = static_cast<const T*>(p.x) + row0 * p.D + c0;
+        const T* dt = static_cast<const T*>(p.dt) + row0 * p.D + c0;
+        const T* z = p.z ? static_cast<const T*>(p.z) + row0 * p.D + c0 : nullptr;
+        const T* gy = static_cast<const T*>(bp.gy) + row0 * p.D + c0;
+        T* dx = static_cast<T*>(bp.dx) + row0 * p.D + c0;
+        T* ddt = static_cast<T*>(bp.ddt) + row0 * p.D + c0;
+        T* dz = static_cast<T*>(bp.dz) + row0 * p.D + c0;
+        const T* cs = p.cs_in ? static_cast<const T*>(p.cs_in) + (size_t)bh * (p.W - 1) * p.D + c0 : nullptr;
+        const size_t grow = (size_t)(b * p.G + h / (p.H / p.G)) * p.T;
+        const T* Bm = static_cast<const T*>(p.Bm) + grow * N;
+        const T* Cm = static_cast<const T*>(p.Cm) + grow * N;
+        // channels cp, cp + 1 of tokens 4 uq .. 4 uq + 3 of a chunk
+        const bool has_unit = tid < UNITS;
+        const int uq = min(tid / (CPB / 2), kQuads - 1), cp = 2 * (tid % (CPB / 2)), pl = cp >> 1;
+        const unsigned off = (unsigned)(4 * uq) * p.D + cp;
+        float w[4][2] = {}, cb[2] = {0.0f, 0.0f}, bias[2] = {0.0f, 0.0f}, feed[2] = {0.0f, 0.0f};
+        float par[kPar][2] = {};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int hc = h * p.D + c0 + cp + e;
-            for (int i = 0; i < p.W; ++i) w[i][e] = p.cw[(size_t)hc * p.W + i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < p.W) w[i][e] = p.cw[(size_t)hc * p.W + i];
             if (p.cb) cb[e] = p.cb[hc];
             if (p.dt_bias) bias[e] = p.dt_bias[hc];
             if (p.dfeed) feed[e] = p.dfeed[hc];
         }
-        if (!LOCAL && uq == 0)
+        if (!LOCAL && has_unit && uq == 0)
             for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<float4*>(sZ[kQuads][pl + e * L::ODD]) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
-    // inputs tq - 3 .. tq + 3 of the unit's channels
-    auto window = [&](int tq, float2* xv) {
+                *reinterpret_cast<float4*>(sm.C5[0][kQuads][pl + e * L::ODD]) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        Raw xr[7], dr[4], gr[4], zr[4], xf[4];
+        // input t of the unit's channels, from before the sequence too
+        auto input = [&](int t) {
+            if (t >= 0) return ldpair(x + (size_t)t * p.D + cp);
+            return cs && t >= 1 - p.W ? ldpair(cs + (size_t)(p.W - 1 + t) * p.D + cp) : Pair<T>::zero();
+        };
+        auto fetch = [&](int k) {
+            if (!has_unit || k >= chunks) return;
+            const int t0 = tlast - k * kSsmChunk, tq = t0 + 4 * uq;
+            const bool in = t0 >= 4 && t0 + kSsmChunk <= end;
+            const T *dtt = dt + (size_t)t0 * p.D, *gyt = gy + (size_t)t0 * p.D, *zt = z + (size_t)t0 * p.D, *xt = x + (size_t)t0 * p.D;
+            if (!LOCAL)
 #pragma unroll
-        for (int i = 0; i < 7; ++i) {
-            const int t = tq - 3 + i;
-            xv[i] = make_float2(0.0f, 0.0f);
-            if (i < 3 && p.W < 4 - i) continue;
-            if (t >= 0) {
-                if (t < end) xv[i] = Pair<T>::f(ldpair(x + (size_t)t * p.D + cp));
-            } else if (cs && t >= 1 - p.W) {
-                xv[i] = Pair<T>::f(ldpair(cs + (size_t)(p.W - 1 + t) * p.D + cp));
-            }
-        }
-    };
-
-    if (end > begin)
-    for (int t0 = begin + (end - begin - 1) / kSsmChunk * kSsmChunk; t0 >= begin; t0 -= kSsmChunk) {
-        if (has_unit) {
-            const int tq = t0 + 4 * uq;
-            float2 xv[7];
-            if (!LOCAL) window(tq, xv);
-            float dv[2][4], uv[2][4], pv[2][4], fv[2][4], sv[2][4];
+                for (int i = 0; i < 7; ++i) {
+                    xr[i] = Pair<T>::zero();
+                    if (i < 3 && p.W < 4 - i) continue;  // 3 - i tokens back: not in the filter
+                    if (in) xr[i] = ldpair(xt + (i - 3) * p.D + off);
+                    else if (tq - 3 + i < end) xr[i] = input(tq - 3 + i);
+                }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool live = tq + j < end;
-                const size_t at = (size_t)(tq + j) * p.D + cp;
-                float2 d = make_float2(0.0f, 0.0f), g = d;
-                if (live) {
-                    d = Pair<T>::f(ldpair(dt + at));
-                    g = Pair<T>::f(ldpair(gy + at));
-                    if (z) {
-                        const float2 zz = Pair<T>::f(ldpair(z + at));
-                        g.x *= silu(zz.x);
-                        g.y *= silu(zz.y);
-                    }
+                const bool live = in || tq + j < end;
+                dr[j] = live ? ldpair(dtt + j * p.D + off) : Pair<T>::zero();
+                gr[j] = live ? ldpair(gyt + j * p.D + off) : Pair<T>::zero();
+                zr[j] = z && live ? ldpair(zt + j * p.D + off) : Pair<T>::zero();
+            }
+        };
+        auto fetch_x = [&](int k) {
+            if (!has_unit) return;
+            const int tq = tlast - k * kSsmChunk + 4 * uq;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xf[j] = tq + j < end ? ldpair(x + (size_t)(tq + j) * p.D + cp) : Pair<T>::zero();
+        };
+        auto copy_bc = [&](int k) {
+            constexpr int PER = 16 / (int)sizeof(T), ROW = N / PER;  // values in 16 bytes, pieces of a token
+            if (k < chunks) {
+                const int t0 = tlast - k * kSsmChunk;
+                for (int i = tid; i < kSsmChunk * ROW; i += EW) {
+                    const bool there = t0 + i / ROW < end;
+                    const size_t at = there ? (size_t)t0 * N + i * PER : 0;
+                    if (!LOCAL) copy16(reinterpret_cast<char*>(&sm.B[k % 3][0][0]) + 16 * i, Bm + at, there);
+                    copy16(reinterpret_cast<char*>(&sm.C[k % 3][0][0]) + 16 * i, Cm + at, there);
                 }
-                float2 f = make_float2(1.0f, 1.0f), u = make_float2(0.0f, 0.0f), sg = f;
-                if (!LOCAL) {
-                    u = xv[3 + j];
-                    if (p.W) {
-                        float2 zc = make_float2(cb[0], cb[1]);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        using Two = float2[2][2];  // [channel][tokens 0 1, 2 3]
+        auto unpack = [&](const Raw* r, Two& o) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 a = Pair<T>::f(r[j]);
+                (&o[0][j >> 1].x)[j & 1] = a.x;
+                (&o[1][j >> 1].x)[j & 1] = a.y;
+            }
+        };
+        auto put = [&](float (&arr)[kQuads][L::PLACES][4], const Two& v) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float4*>(arr[uq][pl + e * L::ODD]) = make_float4(v[e][0].x, v[e][0].y, v[e][1].x, v[e][1].y);
+        };
+        auto get = [&](const float (&arr)[kQuads][L::PLACES][4], Two& v) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float4 a = *reinterpret_cast<const float4*>(arr[uq][pl + e * L::ODD]);
+                v[e][0] = make_float2(a.x, a.y);
+                v[e][1] = make_float2(a.z, a.w);
+            }
+        };
+        auto stage = [&](int k) {
+            if (!has_unit || k >= chunks) return;
+            const int t0 = tlast - k * kSsmChunk, tq = t0 + 4 * uq, m = k & 1;
+            Two d, g;
+            unpack(dr, d);
+            unpack(gr, g);
+            if (p.preact) {
+                Two sg;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 a = add2(d[e][i], two(bias[e]));
+                        d[e][i] = softplus2(a);
+                        if (!LOCAL) sg[e][i] = sigmoid2(a);
+                    }
+                if (!LOCAL) put(sm.S[m], sg);
+            }
+            if (z) {
+                Two zz;
+                unpack(zr, zz);
+                Two gz;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 sg = sigmoid2(zz[e][i]);
+                        if (!LOCAL) gz[e][i] = mul2(g[e][i], dsilu2(zz[e][i], sg));
+                        g[e][i] = mul2(g[e][i], mul2(zz[e][i], sg));
+                    }
+                if (!LOCAL) put(sm.Z[m], gz);
+            }
+            Two u;
+            if (!LOCAL) {
+                if (p.W) {
+                    float2 xv[7];
+#pragma unroll
+                    for (int i = 0; i < 7; ++i) xv[i] = Pair<T>::f(xr[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float z0 = cb[0], z1 = cb[1];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (i < p.W) {
-                                zc.x = fmaf(w[i][0], xv[3 + j - i].x, zc.x);
-                                zc.y = fmaf(w[i][1], xv[3 + j - i].y, zc.y);
+                                z0 = fmaf(w[i][0], xv[3 + j - i].x, z0);
+                                z1 = fmaf(w[i][1], xv[3 + j - i].y, z1);
                             }
-                        u = zc;
-                        if (p.silu) {
-                            const float s0 = sigmoid(zc.x), s1 = sigmoid(zc.y);
-                            u = make_float2(zc.x * s0, zc.y * s1);
-                            f = make_float2(dsilu(zc.x, s0), dsilu(zc.y, s1));
-                        }
+                        (&u[0][j >> 1].x)[j & 1] = z0;
+                        (&u[1][j >> 1].x)[j & 1] = z1;
                     }
+                    if (p.silu) {
+                        Two f;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float2 sg = sigmoid2(u[e][i]);
+                                f[e][i] = dsilu2(u[e][i], sg);
+                                u[e][i] = mul2(u[e][i], sg);
+                            }
+                        put(sm.F[m], f);
+                    }
+                } else {
+                    unpack(xr + 3, u);
+                }
+            }
+            if (t0 + kSsmChunk > end) {  // tokens behind the end: no step, no input, no gradient
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (tq + j >= end) {
+                            (&d[e][j >> 1].x)[j & 1] = 0.0f;
+                            (&g[e][j >> 1].x)[j & 1] = 0.0f;
+                            if (!LOCAL) (&u[e][j >> 1].x)[j & 1] = 0.0f;
+                        }
+            }
+            put(sm.D[m], d);
+            put(sm.P[m], g);
+            if (!LOCAL) put(sm.U[m], u);
+        };
+        // The gradients of dt and z, dzc of the convolution; then, once all of the
+        // chunk's dzc are there, those of x and the taps.
+        auto finish = [&](int k) {
+            const int t0 = tlast - k * kSsmChunk, tq = t0 + 4 * uq, m = k & 1;
+            const bool in = t0 + kSsmChunk <= end;
+            Two zc;
+            if (has_unit) {
+                Two d, u, pp, q, e2, sg;
+                get(sm.D[m], d);
+                get(sm.U[m], u);
+                get(sm.P[m], pp);
+                get(sm.Q[m], q);
+                get(sm.E[m], e2);
+                float ps[3][2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float2 s1 = two(0.0f), s2 = two(0.0f);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        sg[e][i] = fma2(u[e][i], q[e][i], mul2(e2[e][i], two(kLn2)));
+                        zc[e][i] = fma2(d[e][i], q[e][i], mul2(two(feed[e]), pp[e][i]));
+                        s1 = fma2(pp[e][i], u[e][i], s1);
+                    }
+                    ps[1][e] = s1.x + s1.y;
                 }
                 if (p.preact) {
-                    d.x += bias[0];
-                    d.y += bias[1];
-                    if (!LOCAL) sg = make_float2(sigmoid(d.x), sigmoid(d.y));
-                    d = make_float2(softplus(d.x), softplus(d.y));
-                }
-                dv[0][j] = live ? d.x : 0.0f; dv[1][j] = live ? d.y : 0.0f;
-                pv[0][j] = g.x; pv[1][j] = g.y;
-                uv[0][j] = live ? u.x : 0.0f; uv[1][j] = live ? u.y : 0.0f;
-                fv[0][j] = f.x; fv[1][j] = f.y;
-                sv[0][j] = sg.x; sv[1][j] = sg.y;
-            }
+                    get(sm.S[m], e2);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int k = pl + e * L::ODD;
-                *reinterpret_cast<float4*>(sD[uq][k]) = make_float4(dv[e][0], dv[e][1], dv[e][2], dv[e][3]);
-                *reinterpret_cast<float4*>(sP[uq][k]) = make_float4(pv[e][0], pv[e][1], pv[e][2], pv[e][3]);
-                if (!LOCAL) {
-                    *reinterpret_cast<float4*>(sU[uq][k]) = make_float4(uv[e][0], uv[e][1], uv[e][2], uv[e][3]);
-                    *reinterpret_cast<float4*>(sF[uq][k]) = make_float4(fv[e][0], fv[e][1], fv[e][2], fv[e][3]);
-                    *reinterpret_cast<float4*>(sS[uq][k]) = make_float4(sv[e][0], sv[e][1], sv[e][2], sv[e][3]);
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) sg[e][i] = mul2(sg[e][i], e2[e][i]);
+                }
+                if (p.W && p.silu) {
+                    get(sm.F[m], e2);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) zc[e][i] = mul2(zc[e][i], e2[e][i]);
+                }
+                if (!in)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (tq + j >= end) (&sg[e][j >> 1].x)[j & 1] = (&zc[e][j >> 1].x)[j & 1] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 a = add2(sg[e][0], sg[e][1]), c = add2(zc[e][0], zc[e][1]);
+                    ps[0][e] = a.x + a.y;
+                    ps[2][e] = c.x + c.y;
+                    *reinterpret_cast<float4*>(sm.C5[m][uq][pl + e * L::ODD]) = make_float4(zc[e][0].x, zc[e][0].y, zc[e][1].x, zc[e][1].y);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) par[i][e] += ps[i][e];
+                }
+                T* out = ddt + (size_t)t0 * p.D;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in || tq + j < end) stpair(out + j * p.D + off, (&sg[0][j >> 1].x)[j & 1], (&sg[1][j >> 1].x)[j & 1]);
+                if (z) {
+                    Two y, gz;
+                    get(sm.Y[m], y);
+                    get(sm.Z[m], gz);
+                    out = dz + (size_t)t0 * p.D;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) y[e][i] = mul2(fma2(two(feed[e]), u[e][i], y[e][i]), gz[e][i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (in || tq + j < end) stpair(out + j * p.D + off, (&y[0][j >> 1].x)[j & 1], (&y[1][j >> 1].x)[j & 1]);
                 }
             }
-        }
-        for (int i = tid; i < kSsmChunk * N / 4; i += TH) {
-            const int t = t0 + i / (N / 4), n = 4 * (i % (N / 4));
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = v;
-            if (t < end) {
-                u = ld4(Cm + (size_t)t * N + n);
-                if (!LOCAL) v = ld4(Bm + (size_t)t * N + n);
+            part_sync<2, EW>();
+            if (has_unit) {
+                float2 xv[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) xv[j] = Pair<T>::f(xf[j]);
+                float o[2][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float4 n = *reinterpret_cast<const float4*>(sm.C5[m][uq + 1][pl + e * L::ODD]);
+                    const float v[8] = {zc[e][0].x, zc[e][0].y, zc[e][1].x, zc[e][1].y, n.x, n.y, n.z, n.w};
+                    float pw[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        o[e][j] = p.W ? 0.0f : v[j];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i < p.W) {  // token j + i takes tap i of this one
+                                o[e][j] = fmaf(w[i][e], v[j + i], o[e][j]);
+                                pw[i] = fmaf(v[j + i], e ? xv[j].y : xv[j].x, pw[i]);
+                            }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) par[3 + i][e] += pw[i];
+                    if (uq == 0)  // for the chunk before
+                        *reinterpret_cast<float4*>(sm.C5[m ^ 1][kQuads][pl + e * L::ODD]) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = tq + j;
+                    if (t >= end) continue;
+                    if (p.W > 1 && end < len && t >= end - 3) {  // the next segment's dzc are still to be added
+                        float* ed = wk.edge + (((size_t)seg * p.B * p.H + bh) * 2 * 3 + (t - (end - 3))) * p.D + c0 + cp;
+                        ed[0] = o[0][j];
+                        ed[1] = o[1][j];
+                        continue;
+                    }
+                    if (bp.gcs && t >= len - (p.W - 1)) {
+                        const float2 g = Pair<T>::f(ldpair(static_cast<const T*>(bp.gcs) +
+                            ((size_t)bh * (p.W - 1) + t - (len - (p.W - 1))) * p.D + c0 + cp));
+                        o[0][j] += g.x;
+                        o[1][j] += g.y;
+                    }
+                    stpair(dx + (size_t)t * p.D + cp, o[0][j], o[1][j]);
+                }
             }
-            *reinterpret_cast<float4*>(&sC[t - t0][n]) = u;
-            if (!LOCAL) *reinterpret_cast<float4*>(&sB[t - t0][n]) = v;
-        }
+        };
+        copy_bc(0);
+        copy_bc(1);
+        fetch(0);
+        stage(0);
+        fetch(1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
+        for (int k = 0; k <= chunks; ++k) {  // one turn more than the scan warps: the last chunk's gradients
+            if (!LOCAL && k > 0) finish(k - 1);
+            if (k == chunks) break;
+            copy_bc(k + 2);
+            stage(k + 1);
+            fetch(k + 2);
+            if (!LOCAL) fetch_x(k);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // B and C of chunk k + 1 are there
+            __syncthreads();
+        }
+        if (LOCAL) return;
+        if (has_unit) {
+            // the first chunk's dzc (zeros where there is none): what reaches back over the begin
+            const int m = (chunks + 1) & 1;
+            float first[2][3] = {};
+            if (uq == 0 && chunks > 0)
+                for (int e = 0; e < 2; ++e)
+                    for (int j = 0; j < 3; ++j) first[e][j] = sm.C5[m][0][pl + e * L::ODD][j];
+            if (uq == 0 && chunks > 0)
+#pragma unroll
+                for (int r = 1; r < 4; ++r) {  // input r tokens before the begin
+                    if (r >= p.W) continue;
+                    const float2 v = Pair<T>::f(input(begin - r));
+#pragma unroll
+                    for (int i = 1; i < 4; ++i)
+                        if (i >= r && i < p.W) {
+                            par[3 + i][0] = fmaf(first[0][i - r], v.x, par[3 + i][0]);
+                            par[3 + i][1] = fmaf(first[1][i - r], v.y, par[3 + i][1]);
+                        }
+                }
+#pragma unroll
+            for (int i = 0; i < kPar; ++i)
+                for (int e = 0; e < 2; ++e) sm.par[i][uq][cp + e] = par[i][e];
+            if (seg > 0 && begin < len && uq == 0) {  // dzc of the first three tokens, for the end of the segment before
+                float* ed = wk.edge + (((size_t)seg * p.B * p.H + bh) * 2 + 1) * 3 * p.D + c0 + cp;
+                for (int j = 0; j < 3; ++j)
+                    for (int e = 0; e < 2; ++e) ed[(size_t)j * p.D + e] = first[e][j];
+            }
+            if (seg == 0 && bp.dcs && uq == 0)
+                for (int r = 0; r < p.W - 1; ++r) {  // input r - (W-1) before the sequence
+                    float o[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+#pragma unroll
+                        for (int i = 1; i < 4; ++i)
+                            if (j <= r && i == p.W - 1 - r + j) {
+                                o[0] = fmaf(w[i][0], first[0][j], o[0]);
+                                o[1] = fmaf(w[i][1], first[1][j], o[1]);
+                            }
+                    if (bp.gcs && r - len >= 0) {  // a sequence so short that it is carried out again
+                        const float2 g = Pair<T>::f(ldpair(static_cast<const T*>(bp.gcs) +
+                            ((size_t)bh * (p.W - 1) + r - len) * p.D + c0 + cp));
+                        o[0] += g.x;
+                        o[1] += g.y;
+                    }
+                    stpair(static_cast<T*>(bp.dcs) + ((size_t)bh * (p.W - 1) + r) * p.D + c0 + cp, o[0], o[1]);
+                }
+            // rows behind the end have no gradient
+            for (int t = max(begin, len) + uq; t < segend; t += kQuads) {
+                stpair(dx + (size_t)t * p.D + cp, 0.0f, 0.0f);
+                stpair(ddt + (size_t)t * p.D + cp, 0.0f, 0.0f);
+                if (z) stpair(dz + (size_t)t * p.D + cp, 0.0f, 0.0f);
+            }
+        }
+        part_sync<2, EW>();
+        for (int i = tid; i < kPar * CPB; i += EW) {
+            const int k = i / CPB, c = i % CPB;
+            float a = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q) a += sm.par[k][q][c];
+            wk.pPar[((size_t)(seg * p.B + b) * kPar + k) * p.H * p.D + h * p.D + c0 + c] = a;
+        }
+        return;
+    }
+
+    // -------------------------------------------- scan warps
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ch = tid / LPC, sl = tid % LPC, place = L::place(ch);
+    const size_t srow = ((size_t)bh * p.D + c0 + ch) * N + 4 * sl;
+    const size_t nc = (p.T + kSsmChunk - 1) / kSsmChunk;
+    const size_t srow_saved = ((size_t)bh * nc * p.D + c0 + ch) * N + 4 * sl, sstep = (size_t)p.D * N;
+    float2 A2[2], G[2] = {two(0.0f), two(0.0f)}, dA[2] = {two(0.0f), two(0.0f)};
+    float dsum = 0.0f;
+    {
+        const float4 a = ld4(p.A + ((size_t)h * p.D + c0 + ch) * N + 4 * sl);
+        A2[0] = make_float2(a.x * kLog2e, a.y * kLog2e);
+        A2[1] = make_float2(a.z * kLog2e, a.w * kLog2e);
+    }
+    float4 next_state = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!LOCAL) {
+        if (chunks > 0) next_state = *reinterpret_cast<const float4*>(wk.saved + srow_saved + tlast / kSsmChunk * sstep);
+        if (bp.gST) {
+            const float4 v = ld4(bp.gST + srow);
+            G[0] = make_float2(v.x, v.y);
+            G[1] = make_float2(v.z, v.w);
+        }
+        for (int j = wk.P - 1; j > seg; --j) {  // the segments behind this one
+            if (j * wk.len >= len) continue;
+            const float4 v = *reinterpret_cast<const float4*>(wk.local + j * states * N + srow);
+            const float2 ds = two(wk.dsum[j * states + (size_t)bh * p.D + c0 + ch]);
+            G[0] = fma2(ex22(mul2(A2[0], ds)), G[0], make_float2(v.x, v.y));
+            G[1] = fma2(ex22(mul2(A2[1], ds)), G[1], make_float2(v.z, v.w));
+        }
+    }
+    __syncthreads();
+    for (int k = 0; k < chunks; ++k) {
+        const int t0 = tlast - k * kSsmChunk, m = k & 1, m3 = k % 3;
         if (LOCAL) {
 #pragma unroll
             for (int q = kQuads - 1; q >= 0; --q) {
-                const float4 d4 = *reinterpret_cast<const float4*>(sD[q][place]);
-                const float4 p4 = *reinterpret_cast<const float4*>(sP[q][place]);
+                const float4 d4 = *reinterpret_cast<const float4*>(sm.D[m][q][place]);
+                const float4 p4 = *reinterpret_cast<const float4*>(sm.P[m][q][place]);
                 const float dd[4] = {d4.x, d4.y, d4.z, d4.w}, pp[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
                 for (int j = 3; j >= 0; --j) {
-                    const float4 cc = *reinterpret_cast<const float4*>(&sC[4 * q + j][4 * sl]);
-                    G[0] = ex2_fast(dd[j] * A2[0]) * fmaf(cc.x, pp[j], G[0]);
-                    G[1] = ex2_fast(dd[j] * A2[1]) * fmaf(cc.y, pp[j], G[1]);
-                    G[2] = ex2_fast(dd[j] * A2[2]) * fmaf(cc.z, pp[j], G[2]);
-                    G[3] = ex2_fast(dd[j] * A2[3]) * fmaf(cc.w, pp[j], G[3]);
+                    const Quad cq = sm.C[m3][4 * q + j][sl];
+                    const float2 d2 = two(dd[j]), p2 = two(pp[j]);
+                    G[0] = mul2(ex22(mul2(d2, A2[0])), fma2(Four<T>::lo(cq), p2, G[0]));
+                    G[1] = mul2(ex22(mul2(d2, A2[1])), fma2(Four<T>::hi(cq), p2, G[1]));
                     dsum += dd[j];
                 }
             }
@@ -233,72 +535,74 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_bwd_kernel(const SsmBwdParams
             continue;
         }
         // forward over the chunk from its saved state
-        float hist[kSsmChunk][4];
+        float2 hist[kSsmChunk][2];
         {
-            const size_t nc = (p.T + kSsmChunk - 1) / kSsmChunk;
-            const size_t at = (((size_t)bh * nc + t0 / kSsmChunk) * p.D + c0 + ch) * N + 4 * sl;
-            const float4 v = *reinterpret_cast<const float4*>(wk.saved + at);
-            float s[4] = {v.x, v.y, v.z, v.w};
+            float2 s[2] = {make_float2(next_state.x, next_state.y), make_float2(next_state.z, next_state.w)};
+            if (k + 1 < chunks)
+                next_state = *reinterpret_cast<const float4*>(wk.saved + srow_saved + (t0 / kSsmChunk - 1) * sstep);
 #pragma unroll
             for (int q = 0; q < kQuads; ++q) {
-                const float4 d4 = *reinterpret_cast<const float4*>(sD[q][place]);
-                const float4 u4 = *reinterpret_cast<const float4*>(sU[q][place]);
+                const float4 d4 = *reinterpret_cast<const float4*>(sm.D[m][q][place]);
+                const float4 u4 = *reinterpret_cast<const float4*>(sm.U[m][q][place]);
                 const float dd[4] = {d4.x, d4.y, d4.z, d4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
                 float yy[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int t = 4 * q + j;
-                    const float4 bb = *reinterpret_cast<const float4*>(&sB[t][4 * sl]);
-                    const float4 cc = *reinterpret_cast<const float4*>(&sC[t][4 * sl]);
-                    const float du = dd[j] * uu[j];
-                    s[0] = fmaf(ex2_fast(dd[j] * A2[0]), s[0], du * bb.x);
-                    s[1] = fmaf(ex2_fast(dd[j] * A2[1]), s[1], du * bb.y);
-                    s[2] = fmaf(ex2_fast(dd[j] * A2[2]), s[2], du * bb.z);
-                    s[3] = fmaf(ex2_fast(dd[j] * A2[3]), s[3], du * bb.w);
-                    yy[j] = fmaf(s[0], cc.x, fmaf(s[1], cc.y, fmaf(s[2], cc.z, s[3] * cc.w)));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) hist[t][i] = s[i];
+                    const Quad bq = sm.B[m3][t][sl];
+                    const float2 d2 = two(dd[j]), du = two(dd[j] * uu[j]);
+                    s[0] = fma2(ex22(mul2(d2, A2[0])), s[0], mul2(du, Four<T>::lo(bq)));
+                    s[1] = fma2(ex22(mul2(d2, A2[1])), s[1], mul2(du, Four<T>::hi(bq)));
+                    hist[t][0] = s[0];
+                    hist[t][1] = s[1];
+                    if (p.z) {
+                        const Quad cq = sm.C[m3][t][sl];
+                        const float2 v = fma2(s[1], Four<T>::hi(cq), mul2(s[0], Four<T>::lo(cq)));
+                        yy[j] = v.x + v.y;
+                    }
                 }
-                if (z) {
+                if (p.z) {
                     const float r = lane_sum4<LPC>(yy[0], yy[1], yy[2], yy[3]);
-                    if (sl < 4) sY[q][place][sl] = r;
+                    if (sl < 4) sm.Y[m][q][place][sl] = r;
                 }
             }
         }
         // and backwards
-        float dAc[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // this chunk's part: long sums in two steps
+        float2 dAc[2] = {two(0.0f), two(0.0f)};  // this chunk's part: long sums in two steps
 #pragma unroll
         for (int q = kQuads - 1; q >= 0; --q) {
-            const float4 d4 = *reinterpret_cast<const float4*>(sD[q][place]);
-            const float4 u4 = *reinterpret_cast<const float4*>(sU[q][place]);
-            const float4 p4 = *reinterpret_cast<const float4*>(sP[q][place]);
+            const float4 d4 = *reinterpret_cast<const float4*>(sm.D[m][q][place]);
+            const float4 u4 = *reinterpret_cast<const float4*>(sm.U[m][q][place]);
+            const float4 p4 = *reinterpret_cast<const float4*>(sm.P[m][q][place]);
             const float dd[4] = {d4.x, d4.y, d4.z, d4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w},
                         pp[4] = {p4.x, p4.y, p4.z, p4.w};
             float qq[4], ee[4];
 #pragma unroll
             for (int j = 3; j >= 0; --j) {
                 const int t = 4 * q + j;
-                const float4 b4 = *reinterpret_cast<const float4*>(&sB[t][4 * sl]);
-                const float4 c4 = *reinterpret_cast<const float4*>(&sC[t][4 * sl]);
-                const float bb[4] = {b4.x, b4.y, b4.z, b4.w}, cc[4] = {c4.x, c4.y, c4.z, c4.w};
-                const float du = dd[j] * uu[j];
+                const Quad bq = sm.B[m3][t][sl], cq = sm.C[m3][t][sl];
+                const float du1 = dd[j] * uu[j];
+                const float2 d2 = two(dd[j]), p2 = two(pp[j]), du = two(du1), nd = two(-du1);
+                const float2 b2[2] = {Four<T>::lo(bq), Four<T>::hi(bq)}, c2[2] = {Four<T>::lo(cq), Four<T>::hi(cq)};
                 float v[8];
-                float qs = 0.0f, es = 0.0f;
+                float2 qs, es;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    G[i] = fmaf(cc[i], pp[j], G[i]);
-                    qs = fmaf(G[i], bb[i], qs);
-                    const float ww = G[i] * fmaf(-du, bb[i], hist[t][i]);
-                    es = fmaf(ww, A2[i], es);
-                    dAc[i] = fmaf(ww, dd[j], dAc[i]);
-                    v[i] = G[i] * du;
-                    v[4 + i] = pp[j] * hist[t][i];
-                    G[i] *= ex2_fast(dd[j] * A2[i]);
+                for (int i = 0; i < 2; ++i) {
+                    G[i] = fma2(c2[i], p2, G[i]);
+                    qs = i ? fma2(G[i], b2[i], qs) : mul2(G[i], b2[i]);
+                    const float2 ww = mul2(G[i], fma2(nd, b2[i], hist[t][i]));
+                    es = i ? fma2(ww, A2[i], es) : mul2(ww, A2[i]);
+                    dAc[i] = fma2(ww, d2, dAc[i]);
+                    const float2 gb = mul2(G[i], du), gc = mul2(p2, hist[t][i]);
+                    v[2 * i] = gb.x;
+                    v[2 * i + 1] = gb.y;
+                    v[4 + 2 * i] = gc.x;
+                    v[5 + 2 * i] = gc.y;
+                    G[i] = mul2(G[i], decay_again(d2, A2[i]));
                 }
-                qq[j] = qs;
-                ee[j] = es;
+                qq[j] = qs.x + qs.y;
+                ee[j] = es.x + es.y;
                 // over the warp's channels: each step halves what a lane holds
-                const int lane = tid & 31, wrp = tid >> 5;
                 int first = 0, count = 8;
 #pragma unroll
                 for (int o = 16; o >= LPC && o >= 4; o >>= 1) {
@@ -314,7 +618,7 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_bwd_kernel(const SsmBwdParams
                         }
                     first += up ? count : 0;
                 }
-                float* r = &sR[wrp][t % F][(first >> 2) * N + 4 * sl + (first & 3)];
+                float* r = &sm.R[warp][t % F][(first >> 2) * N + 4 * sl + (first & 3)];
                 if (CW == 8) {
                     r[0] = v[0];
                 } else if (CW == 4) {
@@ -324,184 +628,41 @@ __global__ void __launch_bounds__(CPB * N / 4) ssm_bwd_kernel(const SsmBwdParams
                     if (CW == 1) *reinterpret_cast<float4*>(r + N) = make_float4(v[4], v[5], v[6], v[7]);
                 }
                 if (t % F == 0) {  // F tokens are in: the block's sums
-                    __syncthreads();
+                    part_sync<1, TH>();
                     float* out = wk.part + (((size_t)bh * wk.nblk + blk) * p.T + t0 + t) * 2 * N;
-                    for (int i = tid; i < F * 2 * N; i += TH) {
-                        float a = 0.0f;
+                    for (int i = 4 * tid; i < F * 2 * N; i += 4 * TH) {
+                        float4 a = *reinterpret_cast<const float4*>(&sm.R[0][0][0] + i);
 #pragma unroll
-                        for (int k = 0; k < WARPS; ++k) a += (&sR[k][0][0])[i];
-                        if (t0 + t + i / (2 * N) < end) out[i] = a;
+                        for (int o = 1; o < WARPS; ++o) {
+                            const float4 c = *reinterpret_cast<const float4*>(&sm.R[o][0][0] + i);
+                            a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
+                        }
+                        if (t0 + t + i / (2 * N) < end) *reinterpret_cast<float4*>(out + i) = a;
                     }
-                    __syncthreads();
+                    part_sync<1, TH>();
                 }
             }
             const float rq = lane_sum4<LPC>(qq[0], qq[1], qq[2], qq[3]);
             const float re = lane_sum4<LPC>(ee[0], ee[1], ee[2], ee[3]);
             if (sl < 4) {
-                sQ[q][place][sl] = rq;
-                sE[q][place][sl] = re;
+                sm.Q[m][q][place][sl] = rq;
+                sm.E[m][q][place][sl] = re;
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dA[i] += dAc[i];
+        dA[0] = add2(dA[0], dAc[0]);
+        dA[1] = add2(dA[1], dAc[1]);
         __syncthreads();
-        // element-wise: the gradients of dt and z, dzc of the convolution
-        if (has_unit) {
-            const int tq = t0 + 4 * uq;
-            float ps[3][2] = {};
-            float zc[2][4], ddt[2][4], dz[2][4] = {};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int k = pl + e * L::ODD;
-                const float4 D = *reinterpret_cast<const float4*>(sD[uq][k]);
-                const float4 U = *reinterpret_cast<const float4*>(sU[uq][k]);
-                const float4 Pq = *reinterpret_cast<const float4*>(sP[uq][k]);
-                const float4 Q = *reinterpret_cast<const float4*>(sQ[uq][k]);
-                const float4 E = *reinterpret_cast<const float4*>(sE[uq][k]);
-                const float4 Fz = *reinterpret_cast<const float4*>(sF[uq][k]);
-                const float4 S = *reinterpret_cast<const float4*>(sS[uq][k]);
-                const float d[4] = {D.x, D.y, D.z, D.w}, u[4] = {U.x, U.y, U.z, U.w}, pq[4] = {Pq.x, Pq.y, Pq.z, Pq.w},
-                            qv[4] = {Q.x, Q.y, Q.z, Q.w}, ev[4] = {E.x, E.y, E.z, E.w}, f[4] = {Fz.x, Fz.y, Fz.z, Fz.w},
-                            sg[4] = {S.x, S.y, S.z, S.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool live = tq + j < end;
-                    ddt[e][j] = live ? fmaf(u[j], qv[j], ev[j] * kLn2) * sg[j] : 0.0f;
-                    zc[e][j] = live ? fmaf(d[j], qv[j], feed[e] * pq[j]) * f[j] : 0.0f;
-                    ps[0][e] += ddt[e][j];
-                    ps[1][e] = fmaf(pq[j], u[j], ps[1][e]);
-                    ps[2][e] += zc[e][j];
-                }
-                *reinterpret_cast<float4*>(sZ[uq][k]) = make_float4(zc[e][0], zc[e][1], zc[e][2], zc[e][3]);
-                if (z) {
-                    const float4 Yq = *reinterpret_cast<const float4*>(sY[uq][k]);
-                    dz[e][0] = fmaf(feed[e], u[0], Yq.x); dz[e][1] = fmaf(feed[e], u[1], Yq.y);
-                    dz[e][2] = fmaf(feed[e], u[2], Yq.z); dz[e][3] = fmaf(feed[e], u[3], Yq.w);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (tq + j >= end) continue;
-                const size_t at = (size_t)(tq + j) * p.D + cp;
-                stpair(static_cast<T*>(bp.ddt) + row0 * p.D + c0 + at, ddt[0][j], ddt[1][j]);
-                if (z) {
-                    const float2 zz = Pair<T>::f(ldpair(z + at)), g = Pair<T>::f(ldpair(gy + at));
-                    stpair(static_cast<T*>(bp.dz) + row0 * p.D + c0 + at, g.x * dz[0][j] * dsilu(zz.x, sigmoid(zz.x)),
-                           g.y * dz[1][j] * dsilu(zz.y, sigmoid(zz.y)));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                for (int e = 0; e < 2; ++e) par[i][e] += ps[i][e];
-        }
-        __syncthreads();
-        if (has_unit) {  // through the convolution
-            const int tq = t0 + 4 * uq;
-            float2 xv[7];
-            window(tq, xv);
-            float o[2][4], pw[4][2] = {};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int k = pl + e * L::ODD;
-                const float4 a = *reinterpret_cast<const float4*>(sZ[uq][k]);
-                const float4 n = *reinterpret_cast<const float4*>(sZ[uq + 1][k]);
-                const float v[8] = {a.x, a.y, a.z, a.w, n.x, n.y, n.z, n.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    o[e][j] = p.W ? 0.0f : v[j];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < p.W) {
-                            o[e][j] = fmaf(w[i][e], v[j + i], o[e][j]);
-                            pw[i][e] = fmaf(v[j], e ? xv[3 + j - i].y : xv[3 + j - i].x, pw[i][e]);
-                        }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                for (int e = 0; e < 2; ++e) par[3 + i][e] += pw[i][e];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = tq + j;
-                if (t >= end) continue;
-                if (p.W > 1 && end < len && t >= end - 3) {  // the next segment's dzc are still to be added
-                    float* ed = wk.edge + (((size_t)seg * p.B * p.H + bh) * 2 * 3 + (t - (end - 3))) * p.D + c0 + cp;
-                    ed[0] = o[0][j];
-                    ed[1] = o[1][j];
-                    continue;
-                }
-                if (bp.gcs && t >= len - (p.W - 1)) {
-                    const float2 g = Pair<T>::f(ldpair(static_cast<const T*>(bp.gcs) +
-                        ((size_t)bh * (p.W - 1) + t - (len - (p.W - 1))) * p.D + c0 + cp));
-                    o[0][j] += g.x;
-                    o[1][j] += g.y;
-                }
-                stpair(static_cast<T*>(bp.dx) + (row0 + t) * p.D + c0 + cp, o[0][j], o[1][j]);
-            }
-        }
-        __syncthreads();
-        if (has_unit && uq == 0)
-            for (int e = 0; e < 2; ++e) {
-                const int k = pl + e * L::ODD;
-                *reinterpret_cast<float4*>(sZ[kQuads][k]) = *reinterpret_cast<const float4*>(sZ[0][k]);
-            }
-        // sZ's last quad is read again only behind the next chunk's barriers
     }
+    const float4 g4 = make_float4(G[0].x, G[0].y, G[1].x, G[1].y);
     if (LOCAL) {
-        *reinterpret_cast<float4*>(wk.local + seg * states * N + srow) = make_float4(G[0], G[1], G[2], G[3]);
+        *reinterpret_cast<float4*>(wk.local + seg * states * N + srow) = g4;
         if (sl == 0) wk.dsum[seg * states + (size_t)bh * p.D + c0 + ch] = dsum;
         return;
     }
-    // this segment's sums for the weights
+    // this segment's sums for A
     *reinterpret_cast<float4*>(wk.pA + ((size_t)(seg * p.B + b) * p.H * p.D + h * p.D + c0 + ch) * N + 4 * sl) =
-        make_float4(dA[0], dA[1], dA[2], dA[3]);
-    __syncthreads();
-    float* scratch = &sR[0][0][0];  // [kPar][kQuads][CPB]
-    static_assert(kPar * kQuads * CPB <= WARPS * F * 2 * N, "per-channel sums fit the reduction buffer");
-    if (has_unit)
-#pragma unroll
-        for (int i = 0; i < kPar; ++i)
-            for (int e = 0; e < 2; ++e) scratch[(i * kQuads + uq) * CPB + cp + e] = par[i][e];
-    __syncthreads();
-    for (int i = tid; i < kPar * CPB; i += TH) {
-        const int k = i / CPB, c = i % CPB;
-        float a = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kQuads; ++q) a += scratch[(k * kQuads + q) * CPB + c];
-        wk.pPar[((size_t)(seg * p.B + b) * kPar + k) * p.H * p.D + h * p.D + c0 + c] = a;
-    }
-    // dzc of the segment's first three tokens, for the end of the one before
-    if (seg > 0 && begin < len && has_unit && uq == 0) {
-        float* ed = wk.edge + (((size_t)seg * p.B * p.H + bh) * 2 + 1) * 3 * p.D + c0 + cp;
-        for (int j = 0; j < 3; ++j)
-            for (int e = 0; e < 2; ++e) ed[(size_t)j * p.D + e] = sZ[0][pl + e * L::ODD][j];
-    }
-    if (seg == 0) {
-        if (bp.dS0) *reinterpret_cast<float4*>(bp.dS0 + srow) = make_float4(G[0], G[1], G[2], G[3]);
-        if (bp.dcs && has_unit && uq == 0)
-            for (int r = 0; r < p.W - 1; ++r) {  // input r - (W-1) before the sequence
-                float o[2];
-                for (int e = 0; e < 2; ++e) {
-                    o[e] = 0.0f;
-                    if (len > 0)
-                        for (int j = 0; j <= r; ++j) o[e] = fmaf(w[p.W - 1 - r + j][e], sZ[0][pl + e * L::ODD][j], o[e]);
-                }
-                if (bp.gcs && r - len >= 0) {  // a sequence so short that it is carried out again
-                    const float2 g = Pair<T>::f(ldpair(static_cast<const T*>(bp.gcs) +
-                        ((size_t)bh * (p.W - 1) + r - len) * p.D + c0 + cp));
-                    o[0] += g.x;
-                    o[1] += g.y;
-                }
-                stpair(static_cast<T*>(bp.dcs) + ((size_t)bh * (p.W - 1) + r) * p.D + c0 + cp, o[0], o[1]);
-            }
-    }
-    // rows behind the end have no gradient
-    for (int t = max(begin, len) + tid / (CPB / 2); t < segend; t += TH / (CPB / 2)) {
-        const size_t at = (row0 + t) * p.D + c0 + cp;
-        stpair(static_cast<T*>(bp.dx) + at, 0.0f, 0.0f);
-        stpair(static_cast<T*>(bp.ddt) + at, 0.0f, 0.0f);
-        if (z) stpair(static_cast<T*>(bp.dz) + at, 0.0f, 0.0f);
-    }
+        make_float4(dA[0].x, dA[0].y, dA[1].x, dA[1].y);
+    if (seg == 0 && bp.dS0) *reinterpret_cast<float4*>(bp.dS0 + srow) = g4;
 }
 
 // dB, dC: each group's rows of partial sums, in order.  One thread has four
@@ -621,16 +782,26 @@ size_t layout(const SsmBwdParams& bp, BwdWork* wk) {
     return at * 4;
 }
 
-template <typename T, int N, int CPB>
-cudaError_t launch_bwd(const SsmBwdParams& bp, const BwdWork& wk, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((long long)bp.f.B * bp.f.H * wk.nblk);
-    if (wk.P > 1) {
-        ssm_bwd_kernel<T, N, CPB, true><<<dim3(blocks, wk.P - 1), CPB * N / 4, 0, s>>>(bp, wk);
-        const cudaError_t e = cudaGetLastError();
+template <typename T, int N, int CPB, bool LOCAL>
+cudaError_t launch_bwd_pass(const SsmBwdParams& bp, const BwdWork& wk, cudaStream_t s) {
+    auto kern = ssm_bwd_kernel<T, N, CPB, LOCAL>;
+    constexpr int smem = sizeof(BwdSmem<T, N, CPB, LOCAL>);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    ssm_bwd_kernel<T, N, CPB, false><<<dim3(blocks, wk.P), CPB * N / 4, 0, s>>>(bp, wk);
+    const dim3 grid((unsigned)((long long)bp.f.B * bp.f.H * wk.nblk), LOCAL ? wk.P - 1 : wk.P);
+    kern<<<grid, CPB * N / 4 + kEw<CPB>, smem, s>>>(bp, wk);
     return cudaGetLastError();
+}
+
+template <typename T, int N, int CPB>
+cudaError_t launch_bwd(const SsmBwdParams& bp, const BwdWork& wk, cudaStream_t s) {
+    if (wk.P > 1) {
+        const cudaError_t e = launch_bwd_pass<T, N, CPB, true>(bp, wk, s);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_bwd_pass<T, N, CPB, false>(bp, wk, s);
 }
 
 template <typename T>

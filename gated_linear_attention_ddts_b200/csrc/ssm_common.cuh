@@ -57,10 +57,21 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
 __device__ __forceinline__ float2 sigmoid2(float2 x) { return rcp2(add2(ex22(mul2(x, two(-kLog2e))), two(1.0f))); }
 __device__ __forceinline__ float2 silu2(float2 x) { return mul2(x, sigmoid2(x)); }
 __device__ __forceinline__ float softplus(float x) { return softplus2(two(x)).x; }
-__device__ __forceinline__ float sigmoid(float x) { return rcp_fast(1.0f + ex2_fast(-x * kLog2e)); }
-__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
-// d silu(x) / dx = s (1 + x (1 - s))
-__device__ __forceinline__ float dsilu(float x, float s) { return s * fmaf(x, 1.0f - s, 1.0f); }
+__device__ __forceinline__ float silu(float x) { return x * rcp_fast(1.0f + ex2_fast(-x * kLog2e)); }
+// d silu(x) / dx = s (1 + x (1 - s)), s = sigmoid(x)
+
+__device__ __forceinline__ float2 dsilu2(float2 x, float2 s) {
+    const float2 r = make_float2(1.0f - s.x, 1.0f - s.y);
+    return mul2(s, fma2(x, r, two(1.0f)));
+}
+
+// 16 bytes from global into shared memory without passing registers; zeros where
+// `there` is false.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
 
 // Two neighbouring channels of a row.
 template <typename T>
