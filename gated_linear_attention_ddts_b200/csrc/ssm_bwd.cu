@@ -82,7 +82,7 @@ __device__ __forceinline__ void part_sync() {
 // scan warps run chunk k (forward, then backwards), the others finish chunk k - 1
 // and make delta, u and p of chunk k + 1.
 template <typename T, int N, int CPB, bool LOCAL>
-__global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 : CPB * N / 4 > 64 ? 3 : 4)
+__global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 : CPB * N / 4 > 64 ? 2 : 4)
     ssm_bwd_kernel(const SsmBwdParams bp, const BwdWork wk) {
     using L = Lay<N, CPB>;
     using Raw = typename Pair<T>::Raw;
