@@ -6,9 +6,9 @@ of the computation runs in the library's CUDA kernels; there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -526,85 +526,143 @@ def rdm_ska_decode(q, k, v, k_cache, v_cache, pos, *, scale=0.0, advance_pos=Tru
 
 
 # ---------------------------------------------------------------- selective scan
+# A call's arguments go into the C struct by one struct.pack (the layouts are
+# checked against the ctypes structures when the library is loaded): a single
+# token takes a few microseconds on the GPU, less than ctypes spends on thirty
+# fields.
+_SSM = struct.Struct("@10i18PN")
+_SSM_BWD = struct.Struct("@10i18PN15P")
+_SSM_STEP = struct.Struct("@9i13P")
+_Q8_FILL = struct.Struct("@7i7P2i3P")
+_Q8_DECODE = struct.Struct("@7i7Pfi4PiPN")
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+_CODES = {_F32: RDM_F32, _BF16: RDM_BF16}
+_packed = {}
+
+
+def _load_packed(name):
+    """The library's function `name`, taking its arguments as packed bytes."""
+    if not _packed:
+        lib = load()
+        for layout, ty in ((_SSM, SsmArgs), (_SSM_BWD, SsmBwdArgs), (_SSM_STEP, SsmStepArgs), (_Q8_FILL, SkaQ8FillArgs),
+                           (_Q8_DECODE, SkaQ8DecodeArgs)):
+            if layout.size > ctypes.sizeof(ty) or ctypes.sizeof(ty) - layout.size >= 8:
+                raise RuntimeError(f"{ty.__name__}: {ctypes.sizeof(ty)} bytes, packed {layout.size}")
+        for n in ("rdm_ssm_fwd", "rdm_ssm_bwd", "rdm_ssm_step", "rdm_ska_q8_fill", "rdm_ska_q8_decode",
+                  "rdm_ssm_fwd_workspace_size", "rdm_ssm_bwd_workspace_size", "rdm_ska_q8_decode_workspace_size"):
+            fn = lib[n]
+            size = n.endswith("_size")
+            fn.argtypes = [ctypes.c_char_p] if size else [ctypes.c_char_p, _VP]
+            fn.restype = ctypes.c_size_t if size else _I
+            _packed[n] = fn
+    return _packed[name]
+
+
+def _size(name, packed) -> int:
+    n = _load_packed(name + "_workspace_size")(packed)
+    if n == _NO_SIZE:
+        raise RdmError(RDM_ERR_INVALID_ARG, name)
+    return n
+
+
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
+def _launch(name, packed, dev):
+    status = _load_packed(name)(packed, torch._C._cuda_getCurrentRawStream(dev))
+    if status != RDM_OK:
+        raise RdmError(status, name)
+
+
 def _on(stream):
     """Context in which `stream` (torch stream or handle) is the current one, so
     that what a call allocates belongs to the stream it runs on."""
-    if stream is None:
-        return contextlib.nullcontext()
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                              else torch.cuda.ExternalStream(_stream(stream)))
 
 
-def _current(t: torch.Tensor):
+def _current(t, name) -> int:
     """The device of `t`, which has to be the current one: the library launches there."""
     if not isinstance(t, torch.Tensor):
-        raise TypeError("expected a torch.Tensor")
-    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensors passed to the library must be contiguous CUDA tensors")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _arg(t, name, shape, dtype, device):
-    """The pointer of argument `name` (None stays None) after its checks."""
+def _arg(t, name, shape, dtype, dev):
+    """The pointer of argument `name` after its checks; None is a null pointer."""
     if t is None:
-        return None
+        return 0
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == dev and \
+            t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: tensors passed to the library must be contiguous and on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: tensors passed to the library must be contiguous and on cuda:{dev}")
 
 
-def _buffer(t, name, device):
-    """Pointer and bytes of a buffer of which only the size matters."""
-    if not isinstance(t, torch.Tensor):
+def _given(t, name, shape, dtype, dev):
+    """_arg for one that a call cannot do without."""
+    if t is None:
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: tensors passed to the library must be contiguous and on {device}")
+    return _arg(t, name, shape, dtype, dev)
+
+
+def _buffer(t, dev):
+    """Pointer and bytes of a workspace."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace: tensors passed to the library must be contiguous and on cuda:{dev}")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-_F32 = torch.float32
+def _code(t, name):
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype} (float32 or bfloat16)")
+    return code
+
+
+def _width(conv_weight, *states):
+    """Taps of the convolution, 0 without one."""
+    if conv_weight is None:
+        W = 0
+    elif isinstance(conv_weight, torch.Tensor) and conv_weight.dim() == 3:
+        W = conv_weight.shape[-1]
+    else:
+        raise ValueError("conv_weight: expected [H,D,W]")
+    if W == 0 and (conv_weight is not None or any(s is not None for s in states)):
+        raise ValueError("a convolution's bias or state needs conv_weight [H,D,W] with W >= 1")
+    return W
 
 
 def _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
               conv_silu, lengths, gates, y, ST, conv_state_out, saved_states):
-    dev = _current(x)
+    """The fields of rdm_ssm_args up to the workspace, and the device."""
+    dev = _current(x, "x")
     if x.dim() != 4 or A.dim() != 3 or Bm.dim() != 4:
         raise ValueError("x: expected [B,H,T,D], A: [H,D,N], Bm: [B,G,T,N]")
     B, H, T, D = x.shape
-    N, G = A.shape[-1], Bm.shape[1]
-    code, ty = _dtype_code(x), x.dtype
-    if conv_weight is not None and conv_weight.dim() != 3:
-        raise ValueError("conv_weight: expected [H,D,W]")
-    W = conv_weight.shape[-1] if conv_weight is not None else 0
-    if W == 0 and (conv_weight is not None or conv_state_in is not None or conv_state_out is not None):
-        raise ValueError("a convolution's state needs conv_weight [H,D,W] with W >= 1")
-    seq, group, state, chan = (B, H, T, D), (B, G, T, N), (B, H, D, N), (H, D)
-    cstate = (B, H, W - 1, D)
-    a = SsmArgs(B, H, G, T, D, N, W, code, GATES[gates], int(bool(conv_silu)),
-                _arg(x, "x", seq, ty, dev), _arg(dt, "dt", seq, ty, dev), _arg(Bm, "Bm", group, ty, dev),
-                _arg(Cm, "Cm", group, ty, dev), _arg(z, "z", seq, ty, dev), _arg(A, "A", (H, D, N), _F32, dev),
-                _arg(dt_bias, "dt_bias", chan, _F32, dev), _arg(feedthrough, "feedthrough", chan, _F32, dev),
-                _arg(conv_weight, "conv_weight", (H, D, W), _F32, dev), _arg(conv_bias, "conv_bias", chan, _F32, dev),
-                _arg(conv_state_in, "conv_state_in", cstate, ty, dev), _arg(S0, "S0", state, _F32, dev),
-                _arg(lengths, "lengths", (B,), torch.int32, dev), _arg(y, "y", seq, ty, dev),
-                _arg(ST, "ST", state, _F32, dev), _arg(conv_state_out, "conv_state_out", cstate, ty, dev),
-                _arg(saved_states, "saved_states", (B, H, (T + 15) // 16, D, N), _F32, dev), None, 0)
-    return a
-
-
-def _size(fn, a, where) -> int:
-    n = fn(ctypes.byref(a))
-    if n == ctypes.c_size_t(-1).value:
-        raise RdmError(RDM_ERR_INVALID_ARG, where)
-    return int(n)
+    N, G, ty = A.shape[-1], Bm.shape[1], x.dtype
+    W = _width(conv_weight, conv_bias, conv_state_in, conv_state_out)
+    seq, group, state, chan, cstate = (B, H, T, D), (B, G, T, N), (B, H, D, N), (H, D), (B, H, W - 1, D)
+    return (B, H, G, T, D, N, W, _code(x, "x"), GATES[gates], 1 if conv_silu else 0, _arg(x, "x", seq, ty, dev),
+            _given(dt, "dt", seq, ty, dev), _arg(Bm, "Bm", group, ty, dev), _given(Cm, "Cm", group, ty, dev),
+            _arg(z, "z", seq, ty, dev), _arg(A, "A", (H, D, N), _F32, dev), _arg(dt_bias, "dt_bias", chan, _F32, dev),
+            _arg(feedthrough, "feedthrough", chan, _F32, dev), _arg(conv_weight, "conv_weight", (H, D, W), _F32, dev),
+            _arg(conv_bias, "conv_bias", chan, _F32, dev), _arg(conv_state_in, "conv_state_in", cstate, ty, dev),
+            _arg(S0, "S0", state, _F32, dev), _arg(lengths, "lengths", (B,), _I32, dev), _arg(y, "y", seq, ty, dev),
+            _arg(ST, "ST", state, _F32, dev), _arg(conv_state_out, "conv_state_out", cstate, ty, dev),
+            _arg(saved_states, "saved_states", (B, H, (T + 15) // 16, D, N), _F32, dev)), dev
 
 
 def rdm_ssm_saved_states_size(B, H, T, D, N) -> int:
@@ -619,9 +677,9 @@ def rdm_ssm_saved_states(x, A):
 
 
 def rdm_ssm_fwd_workspace_size(x, dt, A, Bm, Cm, *, conv_weight=None, gates="preact") -> int:
-    a = _ssm_args(x, dt, A, Bm, Cm, None, None, None, None, conv_weight, None, None, True, None, gates,
-                  None, None, None, None)
-    return _size(load().rdm_ssm_fwd_workspace_size, a, "rdm_ssm_fwd_workspace_size")
+    a, _ = _ssm_args(x, dt, A, Bm, Cm, None, None, None, None, conv_weight, None, None, True, None, gates,
+                     None, None, None, None)
+    return _size("rdm_ssm_fwd", _SSM.pack(*a, 0, 0))
 
 
 def rdm_ssm_fwd(x, dt, A, Bm, Cm, *, S0=None, z=None, dt_bias=None, feedthrough=None, conv_weight=None,
@@ -637,46 +695,52 @@ def rdm_ssm_fwd(x, dt, A, Bm, Cm, *, S0=None, z=None, dt_bias=None, feedthrough=
     allocated here starts with zeros then).  return_state allocates ST and
     conv_state_out; workspace=False runs without one.  Returns (y, ST or None,
     conv_state_out or None)."""
-    with _on(stream):
-        if y is None:
-            y = torch.empty_like(x) if lengths is None else torch.zeros_like(x)
-        if return_state and ST is None:
-            ST = torch.empty(x.shape[0], *A.shape, dtype=_F32, device=x.device)
-        if return_state and conv_state_out is None and conv_weight is not None:
-            B, H, _, D = x.shape
-            conv_state_out = torch.empty(B, H, conv_weight.shape[-1] - 1, D, dtype=x.dtype, device=x.device)
-        a = _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
-                      conv_silu, lengths, gates, y, ST, conv_state_out, saved_states)
-        if workspace is None:
-            need = _size(load().rdm_ssm_fwd_workspace_size, a, "rdm_ssm_fwd")
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        if workspace is not None and workspace is not False:
-            a.workspace, a.workspace_bytes = _buffer(workspace, "workspace", x.device)
-        _check(load().rdm_ssm_fwd(ctypes.byref(a), _stream(stream)), "rdm_ssm_fwd")
+    if stream is not None:
+        with _on(stream):
+            return rdm_ssm_fwd(x, dt, A, Bm, Cm, S0=S0, z=z, dt_bias=dt_bias, feedthrough=feedthrough,
+                               conv_weight=conv_weight, conv_bias=conv_bias, conv_state_in=conv_state_in,
+                               conv_silu=conv_silu, lengths=lengths, gates=gates, y=y, ST=ST,
+                               conv_state_out=conv_state_out, saved_states=saved_states,
+                               return_state=return_state, workspace=workspace)
+    if y is None:
+        y = torch.empty_like(x) if lengths is None else torch.zeros_like(x)
+    if return_state:
+        B, H, _, D = x.shape
+        if ST is None:
+            ST = torch.empty((B, H, D, A.shape[-1]), dtype=_F32, device=x.device)
+        if conv_state_out is None and conv_weight is not None:
+            conv_state_out = torch.empty((B, H, conv_weight.shape[-1] - 1, D), dtype=x.dtype, device=x.device)
+    a, dev = _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
+                       conv_silu, lengths, gates, y, ST, conv_state_out, saved_states)
+    packed = _SSM.pack(*a, 0, 0)
+    if workspace is None:
+        need = _size("rdm_ssm_fwd", packed)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    if workspace is not None and workspace is not False:
+        packed = _SSM.pack(*a, *_buffer(workspace, dev))
+    _launch("rdm_ssm_fwd", packed, dev)
     return y, ST, conv_state_out
 
 
-def _ssm_bwd_args(a, grad_y, grad_ST, grad_conv_state_out, g, dev):
-    seq, state = (a.B, a.H, a.T, a.D), (a.B, a.H, a.D, a.N)
-    group, chan, cstate = (a.B, a.G, a.T, a.N), (a.H, a.D), (a.B, a.H, a.W - 1, a.D)
-    ty = torch.bfloat16 if a.dtype == RDM_BF16 else _F32
-    if a.W == 0 and grad_conv_state_out is not None:
-        raise ValueError("a convolution's state needs conv_weight [H,D,W] with W >= 1")
-    return SsmBwdArgs(a, _arg(grad_y, "grad_y", seq, ty, dev), _arg(grad_ST, "grad_ST", state, _F32, dev),
-                      _arg(grad_conv_state_out, "grad_conv_state_out", cstate, ty, dev),
-                      _arg(g.get("dx"), "dx", seq, ty, dev), _arg(g.get("ddt"), "ddt", seq, ty, dev),
-                      _arg(g.get("dz"), "dz", seq, ty, dev), _arg(g.get("dB"), "dB", group, ty, dev),
-                      _arg(g.get("dC"), "dC", group, ty, dev), _arg(g.get("dA"), "dA", (a.H, a.D, a.N), _F32, dev),
-                      _arg(g.get("ddt_bias"), "ddt_bias", chan, _F32, dev), _arg(g.get("dfeed"), "dfeed", chan, _F32, dev),
-                      _arg(g.get("dconv_weight"), "dconv_weight", (a.H, a.D, a.W), _F32, dev),
-                      _arg(g.get("dconv_bias"), "dconv_bias", chan, _F32, dev), _arg(g.get("dS0"), "dS0", state, _F32, dev),
-                      _arg(g.get("dconv_state_in"), "dconv_state_in", cstate, ty, dev))
+def _ssm_bwd_args(a, grad_y, grad_ST, grad_conv_state_out, g, ty, dev):
+    """The fields of rdm_ssm_bwd_args behind the forward's."""
+    B, H, G, T, D, N, W = a[:7]
+    seq, state, group, chan, cstate = (B, H, T, D), (B, H, D, N), (B, G, T, N), (H, D), (B, H, W - 1, D)
+    return (_given(grad_y, "grad_y", seq, ty, dev), _arg(grad_ST, "grad_ST", state, _F32, dev),
+            _arg(grad_conv_state_out, "grad_conv_state_out", cstate, ty, dev), _arg(g["dx"], "dx", seq, ty, dev),
+            _arg(g["ddt"], "ddt", seq, ty, dev), _arg(g["dz"], "dz", seq, ty, dev), _arg(g["dB"], "dB", group, ty, dev),
+            _arg(g["dC"], "dC", group, ty, dev), _arg(g["dA"], "dA", (H, D, N), _F32, dev),
+            _arg(g["ddt_bias"], "ddt_bias", chan, _F32, dev), _arg(g["dfeed"], "dfeed", chan, _F32, dev),
+            _arg(g["dconv_weight"], "dconv_weight", (H, D, W), _F32, dev),
+            _arg(g["dconv_bias"], "dconv_bias", chan, _F32, dev), _arg(g["dS0"], "dS0", state, _F32, dev),
+            _arg(g["dconv_state_in"], "dconv_state_in", cstate, ty, dev))
 
 
 def rdm_ssm_bwd_workspace_size(x, dt, A, Bm, Cm, saved_states=None, *, conv_weight=None, gates="preact") -> int:
-    a = _ssm_args(x, dt, A, Bm, Cm, None, None, None, None, conv_weight, None, None, True, None, gates,
-                  None, None, None, saved_states)
-    return _size(load().rdm_ssm_bwd_workspace_size, SsmBwdArgs(a), "rdm_ssm_bwd_workspace_size")
+    a, _ = _ssm_args(x, dt, A, Bm, Cm, None, None, None, None, conv_weight, None, None, True, None, gates,
+                     None, None, None, saved_states)
+    return _size("rdm_ssm_bwd", _SSM_BWD.pack(*a, 0, 0, *([0] * 15)))
 
 
 def rdm_ssm_bwd(x, dt, A, Bm, Cm, grad_y, grad_ST=None, grad_conv_state_out=None, *, S0=None, z=None,
@@ -688,27 +752,30 @@ def rdm_ssm_bwd(x, dt, A, Bm, Cm, grad_y, grad_ST=None, grad_conv_state_out=None
     dconv_bias, dconv_state_in, dS0; those whose input is given are allocated
     with torch if missing, the others are None.  saved_states: the forward's
     (None runs its recurrence again).  Returns the dict."""
-    with _on(stream):
-        g = dict(grads or {})
-        refs = [("dx", x), ("ddt", dt), ("dz", z), ("dB", Bm), ("dC", Cm), ("dA", A), ("ddt_bias", dt_bias),
-                ("dfeed", feedthrough), ("dconv_weight", conv_weight), ("dconv_bias", conv_bias),
-                ("dconv_state_in", conv_state_in), ("dS0", S0)]
-        for n, ref in refs:
-            if g.get(n) is None:
-                g[n] = torch.empty_like(ref) if ref is not None else None
-        a = _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
-                      conv_silu, lengths, gates, None, None, None, saved_states)
-        if a.W == 0 and (g["dconv_weight"] is not None or g["dconv_state_in"] is not None):
-            raise ValueError("gradients of a convolution need conv_weight [H,D,W] with W >= 1")
-        if not isinstance(grad_y, torch.Tensor):
-            raise TypeError("grad_y: expected a torch.Tensor")
-        ba = _ssm_bwd_args(a, grad_y, grad_ST, grad_conv_state_out, g, x.device)
-        if workspace is None:
-            need = _size(load().rdm_ssm_bwd_workspace_size, ba, "rdm_ssm_bwd")
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        if workspace is not None:
-            ba.fwd.workspace, ba.fwd.workspace_bytes = _buffer(workspace, "workspace", x.device)
-        _check(load().rdm_ssm_bwd(ctypes.byref(ba), _stream(stream)), "rdm_ssm_bwd")
+    if stream is not None:
+        with _on(stream):
+            return rdm_ssm_bwd(x, dt, A, Bm, Cm, grad_y, grad_ST, grad_conv_state_out, S0=S0, z=z, dt_bias=dt_bias,
+                               feedthrough=feedthrough, conv_weight=conv_weight, conv_bias=conv_bias,
+                               conv_state_in=conv_state_in, conv_silu=conv_silu, lengths=lengths, gates=gates,
+                               saved_states=saved_states, grads=grads, workspace=workspace)
+    g = dict(grads) if grads else {}
+    for n, ref in (("dx", x), ("ddt", dt), ("dz", z), ("dB", Bm), ("dC", Cm), ("dA", A), ("ddt_bias", dt_bias),
+                   ("dfeed", feedthrough), ("dconv_weight", conv_weight), ("dconv_bias", conv_bias),
+                   ("dconv_state_in", conv_state_in), ("dS0", S0)):
+        if g.get(n) is None:
+            g[n] = None if ref is None else torch.empty_like(ref)
+    a, dev = _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
+                       conv_silu, lengths, gates, None, None, None, saved_states)
+    _width(conv_weight, grad_conv_state_out, g["dconv_weight"], g["dconv_state_in"])
+    b = _ssm_bwd_args(a, grad_y, grad_ST, grad_conv_state_out, g, x.dtype, dev)
+    if workspace is None:
+        need = _size("rdm_ssm_bwd", _SSM_BWD.pack(*a, 0, 0, *b))
+        ws = (0, 0)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    if workspace is not None:
+        ws = _buffer(workspace, dev)
+    _launch("rdm_ssm_bwd", _SSM_BWD.pack(*a, *ws, *b), dev)
     return g
 
 
@@ -717,28 +784,27 @@ def rdm_ssm_step(x, dt, A, Bm, Cm, S, *, z=None, dt_bias=None, feedthrough=None,
     """One token of the selective scan: x, dt, z [B,H,D], Bm, Cm [B,G,N]; S
     [B,H,D,N] float32 and conv_state [B,H,W-1,D] are updated in place.  Returns
     y [B,H,D]."""
-    dev = _current(x)
+    if stream is not None:
+        with _on(stream):
+            return rdm_ssm_step(x, dt, A, Bm, Cm, S, z=z, dt_bias=dt_bias, feedthrough=feedthrough,
+                                conv_weight=conv_weight, conv_bias=conv_bias, conv_state=conv_state,
+                                conv_silu=conv_silu, gates=gates, y=y)
+    dev = _current(x, "x")
     if x.dim() != 3 or A.dim() != 3 or Bm.dim() != 3:
         raise ValueError("x: expected [B,H,D], A: [H,D,N], Bm: [B,G,N]")
-    B, H, D = x.shape
-    N, G = A.shape[-1], Bm.shape[1]
-    W = conv_weight.shape[-1] if conv_weight is not None else 0
-    ty, chan = x.dtype, (H, D)
-    if conv_state is not None and W < 1:
-        raise ValueError("a convolution's state needs conv_weight [H,D,W] with W >= 1")
-    with _on(stream):
-        if y is None:
-            y = torch.empty_like(x)
-        a = SsmStepArgs(B, H, G, D, N, W, _dtype_code(x), GATES[gates], int(bool(conv_silu)),
-                        _arg(x, "x", (B, H, D), ty, dev), _arg(dt, "dt", (B, H, D), ty, dev),
-                        _arg(Bm, "Bm", (B, G, N), ty, dev), _arg(Cm, "Cm", (B, G, N), ty, dev),
-                        _arg(z, "z", (B, H, D), ty, dev), _arg(A, "A", (H, D, N), _F32, dev),
-                        _arg(dt_bias, "dt_bias", chan, _F32, dev), _arg(feedthrough, "feedthrough", chan, _F32, dev),
-                        _arg(conv_weight, "conv_weight", (H, D, W), _F32, dev),
-                        _arg(conv_bias, "conv_bias", chan, _F32, dev), _arg(S, "S", (B, H, D, N), _F32, dev),
-                        _arg(conv_state, "conv_state", (B, H, W - 1, D), ty, dev) if W > 1 else None,
-                        _arg(y, "y", (B, H, D), ty, dev))
-        _check(load().rdm_ssm_step(ctypes.byref(a), _stream(stream)), "rdm_ssm_step")
+    seq = x.shape
+    B, H, D = seq
+    N, G, ty, chan = A.shape[-1], Bm.shape[1], x.dtype, (H, D)
+    W = _width(conv_weight, conv_bias, conv_state)
+    if y is None:
+        y = torch.empty_like(x)
+    _launch("rdm_ssm_step", _SSM_STEP.pack(
+        B, H, G, D, N, W, _code(x, "x"), GATES[gates], 1 if conv_silu else 0, _arg(x, "x", seq, ty, dev),
+        _given(dt, "dt", seq, ty, dev), _arg(Bm, "Bm", (B, G, N), ty, dev), _given(Cm, "Cm", (B, G, N), ty, dev),
+        _arg(z, "z", seq, ty, dev), _arg(A, "A", (H, D, N), _F32, dev), _arg(dt_bias, "dt_bias", chan, _F32, dev),
+        _arg(feedthrough, "feedthrough", chan, _F32, dev), _arg(conv_weight, "conv_weight", (H, D, W), _F32, dev),
+        _arg(conv_bias, "conv_bias", chan, _F32, dev), _given(S, "S", (B, H, D, N), _F32, dev),
+        _arg(conv_state, "conv_state", (B, H, W - 1, D), ty, dev) if W > 1 else 0, _arg(y, "y", seq, ty, dev)), dev)
     return y
 
 
@@ -757,55 +823,60 @@ def rdm_ska_q8_cache(B, H, dk, dv, window, *, block=64, dtype=torch.float8_e4m3f
     return (torch.zeros(B, window, dk, dtype=torch.uint8, **at).view(dtype),
             torch.zeros(B, H, window, dv, dtype=torch.uint8, **at).view(dtype),
             torch.ones(B, nb, **at), torch.ones(B, H, nb, **at),
-            torch.zeros(B, block, dk, dtype=torch.bfloat16, **at),
-            torch.zeros(B, H, block, dv, dtype=torch.bfloat16, **at),
-            torch.zeros(B, dtype=torch.int32, **at))
+            torch.zeros(B, block, dk, dtype=_BF16, **at), torch.zeros(B, H, block, dv, dtype=_BF16, **at),
+            torch.zeros(B, dtype=_I32, **at))
 
 
 def _q8_cache(B, H, dk, dv, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, dev):
+    """The fields of rdm_ska_q8_cache."""
     ty = k_cache.dtype
-    if ty not in _CACHE_TYPES:
+    kind = _CACHE_TYPES.get(ty)
+    if kind is None:
         raise TypeError(f"unsupported cache dtype {ty} (float8_e4m3fn or int8)")
     if k_cache.dim() != 3 or k_tail.dim() != 3 or k_tail.shape[1] < 1:
         raise ValueError("k_cache: expected [B,window,dk], k_tail: [B,block,dk]")
     w, R = k_cache.shape[1], k_tail.shape[1]
-    nb, bf = (w + R - 1) // R, torch.bfloat16
-    return SkaQ8Cache(B, H, dk, dv, w, R, _CACHE_TYPES[ty], _arg(k_cache, "k_cache", (B, w, dk), ty, dev),
-                      _arg(v_cache, "v_cache", (B, H, w, dv), ty, dev), _arg(k_scale, "k_scale", (B, nb), _F32, dev),
-                      _arg(v_scale, "v_scale", (B, H, nb), _F32, dev), _arg(k_tail, "k_tail", (B, R, dk), bf, dev),
-                      _arg(v_tail, "v_tail", (B, H, R, dv), bf, dev), _arg(pos, "pos", (B,), torch.int32, dev))
+    nb = (w + R - 1) // R
+    return (B, H, dk, dv, w, R, kind, _arg(k_cache, "k_cache", (B, w, dk), ty, dev),
+            _given(v_cache, "v_cache", (B, H, w, dv), ty, dev), _given(k_scale, "k_scale", (B, nb), _F32, dev),
+            _given(v_scale, "v_scale", (B, H, nb), _F32, dev), _arg(k_tail, "k_tail", (B, R, dk), _BF16, dev),
+            _given(v_tail, "v_tail", (B, H, R, dv), _BF16, dev), _given(pos, "pos", (B,), _I32, dev))
 
 
 def rdm_ska_q8_fill(k, v, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, *, lengths=None, stream=None):
     """Fills an 8-bit ring cache (rdm_ska_q8_cache) from a prompt's keys
     [B,T,dk] and values [B,H,T,dv] in bf16, as so many decode steps would, and
     sets pos; lengths [B] int32: tokens of each sequence."""
-    dev = _current(k)
+    if stream is not None:
+        with _on(stream):
+            return rdm_ska_q8_fill(k, v, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, lengths=lengths)
+    dev = _current(k, "k")
     if k.dim() != 3 or v.dim() != 4:
         raise ValueError("k: expected [B,T,dk], v: [B,H,T,dv]")
     B, T, dk = k.shape
-    H, dv = v.shape[1], v.shape[3]
-    a = SkaQ8FillArgs(_q8_cache(B, H, dk, dv, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, dev), T,
-                      _dtype_code(k), _arg(k, "k", (B, T, dk), k.dtype, dev), _arg(v, "v", (B, H, T, dv), k.dtype, dev),
-                      _arg(lengths, "lengths", (B,), torch.int32, dev))
-    _check(load().rdm_ska_q8_fill(ctypes.byref(a), _stream(stream)), "rdm_ska_q8_fill")
+    _, H, _, dv = v.shape
+    ty = k.dtype
+    _launch("rdm_ska_q8_fill", _Q8_FILL.pack(
+        *_q8_cache(B, H, dk, dv, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, dev), T, _code(k, "k"),
+        _arg(k, "k", (B, T, dk), ty, dev), _arg(v, "v", (B, H, T, dv), ty, dev),
+        _arg(lengths, "lengths", (B,), _I32, dev)), dev)
 
 
 def _q8_decode_args(q, k, v, cache, scale, o, advance_pos):
-    dev = _current(q)
+    """The fields of rdm_ska_q8_decode_args up to the workspace, and the device."""
+    dev = _current(q, "q")
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q: expected [B,H,dk], v: [B,H,dv]")
     B, H, dk = q.shape
     dv, ty = v.shape[2], q.dtype
-    return SkaQ8DecodeArgs(_q8_cache(B, H, dk, dv, *cache, dev), float(scale), _dtype_code(q),
-                           _arg(q, "q", (B, H, dk), ty, dev), _arg(k, "k", (B, dk), ty, dev),
-                           _arg(v, "v", (B, H, dv), ty, dev), _arg(o, "o", (B, H, dv), ty, dev),
-                           int(bool(advance_pos)), None, 0)
+    return (*_q8_cache(B, H, dk, dv, *cache, dev), float(scale), _code(q, "q"), _arg(q, "q", (B, H, dk), ty, dev),
+            _given(k, "k", (B, dk), ty, dev), _arg(v, "v", (B, H, dv), ty, dev), _arg(o, "o", (B, H, dv), ty, dev),
+            1 if advance_pos else 0), dev
 
 
 def rdm_ska_q8_decode_workspace_size(q, k, v, *cache) -> int:
-    a = _q8_decode_args(q, k, v, cache, 0.0, None, True)
-    return _size(load().rdm_ska_q8_decode_workspace_size, a, "rdm_ska_q8_decode_workspace_size")
+    a, _ = _q8_decode_args(q, k, v, cache, 0.0, None, True)
+    return _size("rdm_ska_q8_decode", _Q8_DECODE.pack(*a, 0, 0))
 
 
 def rdm_ska_q8_decode(q, k, v, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, *, scale=0.0,
@@ -813,16 +884,21 @@ def rdm_ska_q8_decode(q, k, v, k_cache, v_cache, k_scale, v_scale, k_tail, v_tai
     """One SW-SKA decode step over an 8-bit ring cache (rdm_ska_q8_cache),
     updated in place: q [B,H,dk], k [B,dk], v [B,H,dv] bf16.  scale 0 means
     1/sqrt(dk); workspace=False runs without one.  Returns o [B,H,dv]."""
-    with _on(stream):
-        if o is None:
-            o = torch.empty_like(v)
-        a = _q8_decode_args(q, k, v, (k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos), scale, o, advance_pos)
-        if workspace is None:
-            need = _size(load().rdm_ska_q8_decode_workspace_size, a, "rdm_ska_q8_decode")
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        if workspace is not None and workspace is not False:
-            a.workspace, a.workspace_bytes = _buffer(workspace, "workspace", q.device)
-        _check(load().rdm_ska_q8_decode(ctypes.byref(a), _stream(stream)), "rdm_ska_q8_decode")
+    if stream is not None:
+        with _on(stream):
+            return rdm_ska_q8_decode(q, k, v, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, scale=scale,
+                                     advance_pos=advance_pos, o=o, workspace=workspace)
+    if o is None:
+        o = torch.empty_like(v)
+    a, dev = _q8_decode_args(q, k, v, (k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos), scale, o, advance_pos)
+    packed = _Q8_DECODE.pack(*a, 0, 0)
+    if workspace is None:
+        need = _size("rdm_ska_q8_decode", packed)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is not None and workspace is not False:
+        packed = _Q8_DECODE.pack(*a, *_buffer(workspace, dev))
+    _launch("rdm_ska_q8_decode", packed, dev)
     return o
 
 

@@ -865,7 +865,8 @@ Q8Plan plan(const SkaQ8DecodeParams& p) {
     const long long units = (long long)p.c.B * pl.groups;
     // two CTAs an SM; each split of at least 256 slots, in multiples of the largest block
     long long P = units > 0 ? 2LL * sm_count() / units : 1;
-    const long long most = (p.c.window + 255) / 256;  // at most kMostSplits, the window at most 32768
+    // short windows stay whole: a second launch and the join cost more than half a chunk
+    const long long most = p.c.window <= kChunk ? 1 : (p.c.window + 255) / 256;  // at most kMostSplits, the window at most 32768
     if (P > most) P = most;
     if (P < 1) P = 1;
     const int range = (int)((p.c.window + P - 1) / P + 63) / 64 * 64;

@@ -65,14 +65,6 @@ struct BwdSmem {
     float par[kPar][kQuads][CPB];
 };
 
-// The second evaluation of a decay: not to be taken for the first one, whose 64
-// values a thread cannot keep beside the chunk's states.
-__device__ __forceinline__ float2 decay_again(float2 d, float2 a) {
-    float2 r;
-    asm volatile("mul.rn.f32x2 %0, %1, %2;"
-                 : "=l"(reinterpret_cast<uint64_t&>(r)) : "l"(reinterpret_cast<uint64_t&>(d)), "l"(reinterpret_cast<uint64_t&>(a)));
-    return ex22(r);
-}
 template <int ID, int THREADS>
 __device__ __forceinline__ void part_sync() {
     asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
@@ -385,6 +377,10 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int t = tq + j;
+                    if (t0 + kSsmChunk + 3 <= end) {  // no end near
+                        stpair(dx + (size_t)t0 * p.D + j * p.D + off, o[0][j], o[1][j]);
+                        continue;
+                    }
                     if (t >= end) continue;
                     if (p.W > 1 && end < len && t >= end - 3) {  // the next segment's dzc are still to be added
                         float* ed = wk.edge + (((size_t)seg * p.B * p.H + bh) * 2 * 3 + (t - (end - 3))) * p.D + c0 + cp;
@@ -534,72 +530,81 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
             __syncthreads();
             continue;
         }
-        // forward over the chunk from its saved state
-        float2 hist[kSsmChunk][2];
-        {
-            float2 s[2] = {make_float2(next_state.x, next_state.y), make_float2(next_state.z, next_state.w)};
-            if (k + 1 < chunks)
-                next_state = *reinterpret_cast<const float4*>(wk.saved + srow_saved + (t0 / kSsmChunk - 1) * sstep);
+        // First the states before each four tokens (kept, 12 registers), then for each
+        // four tokens, the last first, their states forward (16 registers) and back.
+        // (With all sixteen states kept the code of a chunk outgrew the instruction
+        // cache and 168 registers left two blocks an SM: 430 us against 370 of the
+        // training step.)
+        float2 before[kQuads][2];
+        before[0][0] = make_float2(next_state.x, next_state.y);
+        before[0][1] = make_float2(next_state.z, next_state.w);
+        if (k + 1 < chunks)
+            next_state = *reinterpret_cast<const float4*>(wk.saved + srow_saved + (t0 / kSsmChunk - 1) * sstep);
 #pragma unroll
-            for (int q = 0; q < kQuads; ++q) {
-                const float4 d4 = *reinterpret_cast<const float4*>(sm.D[m][q][place]);
-                const float4 u4 = *reinterpret_cast<const float4*>(sm.U[m][q][place]);
-                const float dd[4] = {d4.x, d4.y, d4.z, d4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
-                float yy[4];
+        for (int q = 0; q < kQuads - 1; ++q) {
+            const float4 d4 = *reinterpret_cast<const float4*>(sm.D[m][q][place]);
+            const float4 u4 = *reinterpret_cast<const float4*>(sm.U[m][q][place]);
+            const float dd[4] = {d4.x, d4.y, d4.z, d4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
+            float2 s[2] = {before[q][0], before[q][1]};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = 4 * q + j;
-                    const Quad bq = sm.B[m3][t][sl];
-                    const float2 d2 = two(dd[j]), du = two(dd[j] * uu[j]);
-                    s[0] = fma2(ex22(mul2(d2, A2[0])), s[0], mul2(du, Four<T>::lo(bq)));
-                    s[1] = fma2(ex22(mul2(d2, A2[1])), s[1], mul2(du, Four<T>::hi(bq)));
-                    hist[t][0] = s[0];
-                    hist[t][1] = s[1];
-                    if (p.z) {
-                        const Quad cq = sm.C[m3][t][sl];
-                        const float2 v = fma2(s[1], Four<T>::hi(cq), mul2(s[0], Four<T>::lo(cq)));
-                        yy[j] = v.x + v.y;
-                    }
-                }
-                if (p.z) {
-                    const float r = lane_sum4<LPC>(yy[0], yy[1], yy[2], yy[3]);
-                    if (sl < 4) sm.Y[m][q][place][sl] = r;
-                }
+            for (int j = 0; j < 4; ++j) {
+                const Quad bq = sm.B[m3][4 * q + j][sl];
+                const float2 d2 = two(dd[j]), du = two(dd[j] * uu[j]);
+                s[0] = fma2(ex22(mul2(d2, A2[0])), s[0], mul2(du, Four<T>::lo(bq)));
+                s[1] = fma2(ex22(mul2(d2, A2[1])), s[1], mul2(du, Four<T>::hi(bq)));
             }
+            before[q + 1][0] = s[0];
+            before[q + 1][1] = s[1];
         }
-        // and backwards
         float2 dAc[2] = {two(0.0f), two(0.0f)};  // this chunk's part: long sums in two steps
-#pragma unroll
+#pragma unroll 1
         for (int q = kQuads - 1; q >= 0; --q) {
             const float4 d4 = *reinterpret_cast<const float4*>(sm.D[m][q][place]);
             const float4 u4 = *reinterpret_cast<const float4*>(sm.U[m][q][place]);
             const float4 p4 = *reinterpret_cast<const float4*>(sm.P[m][q][place]);
             const float dd[4] = {d4.x, d4.y, d4.z, d4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w},
                         pp[4] = {p4.x, p4.y, p4.z, p4.w};
-            float qq[4], ee[4];
+            float2 s[2] = {before[0][0], before[0][1]};
+#pragma unroll
+            for (int i = 1; i < kQuads; ++i)
+                if (q == i) s[0] = before[i][0], s[1] = before[i][1];
+            float2 hist[4][2], dec[4][2];
+            float yy[4], qq[4], ee[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const Quad bq = sm.B[m3][4 * q + j][sl];
+                const float2 d2 = two(dd[j]), du = two(dd[j] * uu[j]);
+                dec[j][0] = ex22(mul2(d2, A2[0]));
+                dec[j][1] = ex22(mul2(d2, A2[1]));
+                s[0] = fma2(dec[j][0], s[0], mul2(du, Four<T>::lo(bq)));
+                s[1] = fma2(dec[j][1], s[1], mul2(du, Four<T>::hi(bq)));
+                hist[j][0] = s[0];
+                hist[j][1] = s[1];
+            }
 #pragma unroll
             for (int j = 3; j >= 0; --j) {
-                const int t = 4 * q + j;
-                const Quad bq = sm.B[m3][t][sl], cq = sm.C[m3][t][sl];
+                const Quad bq = sm.B[m3][4 * q + j][sl], cq = sm.C[m3][4 * q + j][sl];
                 const float du1 = dd[j] * uu[j];
                 const float2 d2 = two(dd[j]), p2 = two(pp[j]), du = two(du1), nd = two(-du1);
                 const float2 b2[2] = {Four<T>::lo(bq), Four<T>::hi(bq)}, c2[2] = {Four<T>::lo(cq), Four<T>::hi(cq)};
                 float v[8];
-                float2 qs, es;
+                float2 qs, es, ys;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
+                    ys = i ? fma2(hist[j][i], c2[i], ys) : mul2(hist[j][i], c2[i]);
                     G[i] = fma2(c2[i], p2, G[i]);
                     qs = i ? fma2(G[i], b2[i], qs) : mul2(G[i], b2[i]);
-                    const float2 ww = mul2(G[i], fma2(nd, b2[i], hist[t][i]));
+                    const float2 ww = mul2(G[i], fma2(nd, b2[i], hist[j][i]));
                     es = i ? fma2(ww, A2[i], es) : mul2(ww, A2[i]);
                     dAc[i] = fma2(ww, d2, dAc[i]);
-                    const float2 gb = mul2(G[i], du), gc = mul2(p2, hist[t][i]);
+                    const float2 gb = mul2(G[i], du), gc = mul2(p2, hist[j][i]);
                     v[2 * i] = gb.x;
                     v[2 * i + 1] = gb.y;
                     v[4 + 2 * i] = gc.x;
                     v[5 + 2 * i] = gc.y;
-                    G[i] = mul2(G[i], decay_again(d2, A2[i]));
+                    G[i] = mul2(G[i], dec[j][i]);
                 }
+                yy[j] = ys.x + ys.y;
                 qq[j] = qs.x + qs.y;
                 ee[j] = es.x + es.y;
                 // over the warp's channels: each step halves what a lane holds
@@ -618,7 +623,7 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
                         }
                     first += up ? count : 0;
                 }
-                float* r = &sm.R[warp][t % F][(first >> 2) * N + 4 * sl + (first & 3)];
+                float* r = &sm.R[warp][(4 * q + j) % F][(first >> 2) * N + 4 * sl + (first & 3)];
                 if (CW == 8) {
                     r[0] = v[0];
                 } else if (CW == 4) {
@@ -627,9 +632,10 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
                     *reinterpret_cast<float4*>(r) = make_float4(v[0], v[1], v[2], v[3]);
                     if (CW == 1) *reinterpret_cast<float4*>(r + N) = make_float4(v[4], v[5], v[6], v[7]);
                 }
-                if (t % F == 0) {  // F tokens are in: the block's sums
+                if (F < 4 ? j % F == 0 : j == 0 && 4 * q % F == 0) {  // F tokens are in: the block's sums
                     part_sync<1, TH>();
-                    float* out = wk.part + (((size_t)bh * wk.nblk + blk) * p.T + t0 + t) * 2 * N;
+                    const int tf = t0 + 4 * q + j;
+                    float* out = wk.part + (((size_t)bh * wk.nblk + blk) * p.T + tf) * 2 * N;
                     for (int i = 4 * tid; i < F * 2 * N; i += 4 * TH) {
                         float4 a = *reinterpret_cast<const float4*>(&sm.R[0][0][0] + i);
 #pragma unroll
@@ -637,16 +643,18 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
                             const float4 c = *reinterpret_cast<const float4*>(&sm.R[o][0][0] + i);
                             a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
                         }
-                        if (t0 + t + i / (2 * N) < end) *reinterpret_cast<float4*>(out + i) = a;
+                        if (tf + i / (2 * N) < end) *reinterpret_cast<float4*>(out + i) = a;
                     }
                     part_sync<1, TH>();
                 }
             }
             const float rq = lane_sum4<LPC>(qq[0], qq[1], qq[2], qq[3]);
             const float re = lane_sum4<LPC>(ee[0], ee[1], ee[2], ee[3]);
+            const float ry = lane_sum4<LPC>(yy[0], yy[1], yy[2], yy[3]);
             if (sl < 4) {
                 sm.Q[m][q][place][sl] = rq;
                 sm.E[m][q][place][sl] = re;
+                sm.Y[m][q][place][sl] = ry;
             }
         }
         dA[0] = add2(dA[0], dAc[0]);
