@@ -43,16 +43,28 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return y;
 }
 __device__ __forceinline__ float2 rcp2(float2 x) { return make_float2(rcp_fast(x.x), rcp_fast(x.y)); }
+__device__ __forceinline__ float max0(float x) {  // NaN stays NaN
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float2 softplus2(float2 x) {
-    const float2 y = ex22(make_float2(-fabsf(x.x) * kLog2e, -fabsf(x.y) * kLog2e));
+    // e^-|x| = 2^t (1 + r ln 2), t the rounded product |x| log2 e and r what the
+    // rounding left: near |x| = 7 that is 4e-7 of the result, and of a small step.
+    // (|x| up to 200 only, where e^-|x| is 0 in any case and r stays finite.)
+    const float2 a = make_float2(fmaxf(-fabsf(x.x), -200.0f), fmaxf(-fabsf(x.y), -200.0f));
+    const float2 t = mul2(a, two(kLog2e));
+    const float2 r = fma2(a, two(1.925963033500644e-08f), fma2(a, two(kLog2e), make_float2(-t.x, -t.y)));
+    float2 y = ex22(t);
+    y = fma2(y, mul2(r, two(kLn2)), y);
     const float2 s = mul2(y, rcp2(add2(y, two(2.0f))));
     const float2 q = mul2(s, s);
-    float2 r = two(0.2817833423614502f);
-    r = fma2(r, q, two(0.27960604429244995f));
-    r = fma2(r, q, two(0.40024909377098083f));
-    r = fma2(r, q, two(0.6666631698608398f));
-    r = fma2(r, q, two(2.0f));
-    return fma2(s, r, make_float2(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f)));  // NaN comes through s
+    float2 v = two(0.2817833423614502f);
+    v = fma2(v, q, two(0.27960604429244995f));
+    v = fma2(v, q, two(0.40024909377098083f));
+    v = fma2(v, q, two(0.6666631698608398f));
+    v = fma2(v, q, two(2.0f));
+    return fma2(s, v, make_float2(max0(x.x), max0(x.y)));
 }
 __device__ __forceinline__ float2 sigmoid2(float2 x) { return rcp2(add2(ex22(mul2(x, two(-kLog2e))), two(1.0f))); }
 __device__ __forceinline__ float2 silu2(float2 x) { return mul2(x, sigmoid2(x)); }
