@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 2 
                 for (int j = 0; j < 4; ++j) {
                     const Quad bq = sB[m3][4 * q + j][sl];
                     const float2 d2 = two(dd[j]), du = two(dd[j] * uu[j]);
-                    s[0] = fma2(ex22(mul2(d2, A2[0])), s[0], mul2(du, Four<T>::lo(bq)));
-                    s[1] = fma2(ex22(mul2(d2, A2[1])), s[1], mul2(du, Four<T>::hi(bq)));
+                    s[0] = fma2(decay2(d2, A2[0]), s[0], mul2(du, Four<T>::lo(bq)));
+                    s[1] = fma2(decay2(d2, A2[1]), s[1], mul2(du, Four<T>::hi(bq)));
                     if (LOCAL) {
                         dsum += dd[j];
                     } else {
@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmStepPar
             const float4 v = sm[r][ch];
             const Quad bb = sB[(r * HB + hh) * LPC + sl], cc = sC[(r * HB + hh) * LPC + sl];
             const float2 d2 = two(v.x), du = two(v.x * v.y);
-            const float2 lo = fma2(ex22(mul2(d2, A2[0])), make_float2(s4[r].x, s4[r].y), mul2(du, Four<T>::lo(bb)));
-            const float2 hi = fma2(ex22(mul2(d2, A2[1])), make_float2(s4[r].z, s4[r].w), mul2(du, Four<T>::hi(bb)));
+            const float2 lo = fma2(decay2(d2, A2[0]), make_float2(s4[r].x, s4[r].y), mul2(du, Four<T>::lo(bb)));
+            const float2 hi = fma2(decay2(d2, A2[1]), make_float2(s4[r].z, s4[r].w), mul2(du, Four<T>::hi(bb)));
             const float2 t = fma2(hi, Four<T>::hi(cc), mul2(lo, Four<T>::lo(cc)));
             y[r - q] = t.x + t.y;
             if (hc < hd && b0 + r < p.B) *reinterpret_cast<float4*>(S + r * next) = make_float4(lo.x, lo.y, hi.x, hi.y);

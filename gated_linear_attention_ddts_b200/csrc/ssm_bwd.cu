@@ -522,8 +522,8 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
                 for (int j = 3; j >= 0; --j) {
                     const Quad cq = sm.C[m3][4 * q + j][sl];
                     const float2 d2 = two(dd[j]), p2 = two(pp[j]);
-                    G[0] = mul2(ex22(mul2(d2, A2[0])), fma2(Four<T>::lo(cq), p2, G[0]));
-                    G[1] = mul2(ex22(mul2(d2, A2[1])), fma2(Four<T>::hi(cq), p2, G[1]));
+                    G[0] = mul2(decay2(d2, A2[0]), fma2(Four<T>::lo(cq), p2, G[0]));
+                    G[1] = mul2(decay2(d2, A2[1]), fma2(Four<T>::hi(cq), p2, G[1]));
                     dsum += dd[j];
                 }
             }
@@ -550,8 +550,8 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
             for (int j = 0; j < 4; ++j) {
                 const Quad bq = sm.B[m3][4 * q + j][sl];
                 const float2 d2 = two(dd[j]), du = two(dd[j] * uu[j]);
-                s[0] = fma2(ex22(mul2(d2, A2[0])), s[0], mul2(du, Four<T>::lo(bq)));
-                s[1] = fma2(ex22(mul2(d2, A2[1])), s[1], mul2(du, Four<T>::hi(bq)));
+                s[0] = fma2(decay2(d2, A2[0]), s[0], mul2(du, Four<T>::lo(bq)));
+                s[1] = fma2(decay2(d2, A2[1]), s[1], mul2(du, Four<T>::hi(bq)));
             }
             before[q + 1][0] = s[0];
             before[q + 1][1] = s[1];
@@ -574,8 +574,8 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
             for (int j = 0; j < 4; ++j) {
                 const Quad bq = sm.B[m3][4 * q + j][sl];
                 const float2 d2 = two(dd[j]), du = two(dd[j] * uu[j]);
-                dec[j][0] = ex22(mul2(d2, A2[0]));
-                dec[j][1] = ex22(mul2(d2, A2[1]));
+                dec[j][0] = decay2(d2, A2[0]);
+                dec[j][1] = decay2(d2, A2[1]);
                 s[0] = fma2(dec[j][0], s[0], mul2(du, Four<T>::lo(bq)));
                 s[1] = fma2(dec[j][1], s[1], mul2(du, Four<T>::hi(bq)));
                 hist[j][0] = s[0];

@@ -127,6 +127,19 @@ def test_rows_behind_the_end_are_left(cuda_ok):
         ref.assert_near(got[n], t, 50 + 16 + 64, n, grad=True)
 
 
+def test_steps_of_zero_keep_the_state(cuda_ok):
+    """Decays of exactly 1: a sequence that ends inside a tile has the state of its
+    last token, and steps of zero leave a state bit by bit."""
+    i = cuda(ref.inputs(1, 2, 50, 32, 16, seed=13, gates="activated"))
+    ln = torch.tensor([20], dtype=torch.int32, device="cuda")
+    _, ST, _ = call(rdm.rdm_ssm_fwd, i, gates="activated", lengths=ln, return_state=True)
+    head = {n: (t[:, :, :20].contiguous() if n in ("x", "dt", "z", "Bm", "Cm") else t) for n, t in i.items()}
+    _, ST1, _ = call(rdm.rdm_ssm_fwd, head, gates="activated", return_state=True)
+    assert torch.equal(ST, ST1)
+    _, ST2, _ = call(rdm.rdm_ssm_fwd, {**i, "dt": torch.zeros_like(i["dt"])}, gates="activated", return_state=True)
+    assert torch.equal(ST2, i["S0"])
+
+
 @pytest.mark.parametrize("lengths,clamped", [([-3, 9], [0, 9]), ([40, 100], [40, 40])])
 def test_length_out_of_range_is_reported(cuda_ok, lengths, clamped):
     i = ref.inputs(2, 1, 40, 16, 16, seed=1)
