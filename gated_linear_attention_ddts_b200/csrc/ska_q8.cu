@@ -395,25 +395,57 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, l4 = lane & 3;
     const int group = blockIdx.x % pl.groups, b = blockIdx.x / pl.groups, split = blockIdx.y;
     const int h0 = group * pl.G, nh = min(pl.G, c.H - h0);
-    const int pos = c.pos[b];
-    if (pl.cluster) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // pos is read
     const int w = c.window, R = c.block, nb = (w + R - 1) / R, rs = 31 - __clz(R);
+    const int s0 = split * pl.range, wend = min(s0 + pl.range, w);  // this split's slots
+    const size_t bh0 = (size_t)b * c.H + h0;
+    // this warp's head: several warps share one where there are few
+    const int wph = kWarps / nh, hd = min(warp / wph, nh - 1), sub = warp % wph;
+    const bool busy = warp < wph * nh;
+    const unsigned char* kc = c.k + (size_t)b * w * DK;
+    const unsigned char* vc = c.v + (bh0 + hd) * w * DV;
+
+    // What does not depend on the position is asked for before it is known: the
+    // queries, the first chunk's scales and its key tiles (those behind the last
+    // token too; their scores are not taken).
+    const int pos = c.pos[b];
+    uint4 q4 = make_uint4(0, 0, 0, 0);
+    if (tid < nh * (DK / 8)) q4 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + bh0 * DK)[tid];
+    float ks_next, vs_next;  // a block a lane (32 of 16 slots at most)
+    auto fetch_scales = [&](int c0) {
+        const int blk = (c0 >> rs) + lane;
+        ks_next = blk < nb ? c.k_scale[(size_t)b * nb + blk] : 1.0f;
+        vs_next = warp < nh && blk < nb ? c.v_scale[(bh0 + warp) * nb + blk] : 1.0f;
+    };
+    fetch_scales(s0);
+    // This warp's tiles in the order in which it takes them: of each chunk first the
+    // keys' (every eighth tile), then the values' (every wph-th).
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp][0]);
+    constexpr uint32_t TILE = sizeof(sm.ring[0][0]);
+    int pc = s0, pk = s0 + 16 * warp, pv = s0 + 16 * sub;  // the next to ask for
+    uint32_t slot_in = ring, slot_out = ring;
+    auto ask_key = [&]() {
+        if (pk + 16 > w) copy_edge<DK, true>(slot_in, kc, pk, pk, w);
+        else copy_tile<DK, true>(slot_in, kc + (size_t)pk * DK);
+        pk += 16 * kWarps;
+        slot_in = slot_in == ring + (kRing - 1) * TILE ? ring : slot_in + TILE;
+    };
+    int asked = 0;
+    for (; asked < kRing && pk < min(s0 + kChunk, wend); ++asked) {
+        ask_key();
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
+    if (pl.cluster) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // pos is read
     const int n = pos < 0 ? 0 : pos < w ? pos + 1 : w;
     const int cur = pos < 0 ? 0 : pos % w, at = cur & ~(R - 1), fill = cur - at;
-    const int s0 = split * pl.range, s1 = min(s0 + pl.range, n);
+    const int s1 = min(wend, n);
     const bool tail_here = pos >= 0 && at >= s0 && at < s0 + pl.range;
     if (pos < 0 && tid == 0) atomicOr(p.err, kErrBadValue);
-    const size_t bh0 = (size_t)b * c.H + h0;
     const __nv_bfloat16* kin = static_cast<const __nv_bfloat16*>(p.k) + (size_t)b * DK;
     const __nv_bfloat16* vin = static_cast<const __nv_bfloat16*>(p.v) + bh0 * DV;
     __nv_bfloat16* kt = static_cast<__nv_bfloat16*>(c.k_tail) + (size_t)b * R * DK;
     __nv_bfloat16* vt = static_cast<__nv_bfloat16*>(c.v_tail) + bh0 * R * DV;
-    const unsigned char* kc = c.k + (size_t)b * w * DK;
 
-    // this warp's head: several warps share one where there are few
-    const int wph = kWarps / nh, hd = min(warp / wph, nh - 1), sub = warp % wph;
-    const bool busy = warp < wph * nh;
-    const unsigned char* vc = c.v + (bh0 + hd) * w * DV;
     float m = -INFINITY, m2 = -3e38f, l = 0.0f;  // m of the scores, m2 with the scales in them
     float acc[MT][4];
 #pragma unroll
@@ -421,42 +453,35 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
 
-    // This warp's tiles in the order in which it takes them: of each chunk first the
-    // keys' (every eighth tile), then the values' (every wph-th).  An edge tile holds
-    // slots of the block being written or behind the last token.
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp][0]);
-    constexpr uint32_t TILE = sizeof(sm.ring[0][0]);
-    int pc = s0, pk = s0 + 16 * warp, pv = s0 + 16 * sub;  // the next to ask for
-    uint32_t slot_in = ring, slot_out = ring;
+    // An edge tile holds slots of the block being written or behind the last token.
     auto is_edge = [&](int t0) { return (t0 & ~(R - 1)) == at || t0 + 16 > s1; };
     auto bounds = [&](int t0, int& lo, int& hi) {  // slots of a tile that are in the cache
         lo = (t0 & ~(R - 1)) == at ? max(t0, cur + 1) : t0;
         hi = min(t0 + 16, s1);
     };
+    auto next_chunk = [&]() {
+        pc += kChunk;
+        pk = pc + 16 * warp;
+        pv = pc + 16 * sub;
+    };
     auto ask = [&]() {
-        const int c1 = min(pc + kChunk, s1);
-        if (pk < c1 || (busy && pv < c1)) {
-            const bool key = pk < c1;
-            const int t0 = key ? pk : pv;
-            if (is_edge(t0)) {
-                int lo, hi;
-                bounds(t0, lo, hi);
-                if (lo >= hi) lo = t0, hi = s1;  // none of them: copied and not used
-                if (key) copy_edge<DK, true>(slot_in, kc, t0, lo, hi);
-                else copy_edge<DV, false>(slot_in, vc, t0, lo, hi);
-            } else if (key) {
-                copy_tile<DK, true>(slot_in, kc + (size_t)t0 * DK);
-            } else {
-                copy_tile<DV, false>(slot_in, vc + (size_t)t0 * DV);
+        if (pc < s1) {
+            const int c1 = min(pc + kChunk, s1), ke = min(pc + kChunk, wend);
+            if (pk < ke) {
+                ask_key();
+            } else if (busy && pv < c1) {
+                if (is_edge(pv)) {
+                    int lo, hi;
+                    bounds(pv, lo, hi);
+                    if (lo >= hi) lo = pv, hi = s1;  // none of them: copied and not used
+                    copy_edge<DV, false>(slot_in, vc, pv, lo, hi);
+                } else {
+                    copy_tile<DV, false>(slot_in, vc + (size_t)pv * DV);
+                }
+                pv += 16 * wph;
+                slot_in = slot_in == ring + (kRing - 1) * TILE ? ring : slot_in + TILE;
             }
-            if (key) pk += 16 * kWarps;
-            else pv += 16 * wph;
-            slot_in = slot_in == ring + (kRing - 1) * TILE ? ring : slot_in + TILE;
-            if (pk >= c1 && (!busy || pv >= c1)) {  // on to the next chunk
-                pc += kChunk;
-                pk = pc + 16 * warp;
-                pv = pc + 16 * sub;
-            }
+            if (pk >= ke && (!busy || pv >= c1)) next_chunk();
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -469,8 +494,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
     };
 
     if (s0 < s1) {
-#pragma unroll 1
-        for (int i = 0; i < kRing; ++i) ask();
+        if (!busy && pk >= min(pc + kChunk, wend)) next_chunk();
+        for (; asked < kRing; ++asked) ask();
         // the new token's row of the tail (read from the inputs below), and the rows
         // before it toward L2
         if (tail_here) {
@@ -489,12 +514,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
         }
         // queries: as they are for the tail, and as f16 for the codes, each head's
         // times a power of two that puts its largest near 2^14 (exact)
-        for (int i = tid; i < kWarps * DK / 8; i += kDecThreads) {
-            const int hh = i / (DK / 8), x = i % (DK / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (hh < nh) v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (bh0 + hh) * DK)[x];
-            reinterpret_cast<uint4*>(qs[hh])[x] = v;
-        }
+        if (tid < kWarps * (DK / 8)) reinterpret_cast<uint4*>(qs[tid / (DK / 8)])[tid % (DK / 8)] = q4;
         if (tid < 16) sm.zero[tid] = __half(0.0f);
         __syncthreads();
         // lane's dimensions of a row: 16 l4 .. + 15, and 64 more on for d_k = 128; heads by g
@@ -531,14 +551,14 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
 
         for (int c0 = s0; c0 < s1; c0 += kChunk) {
             const int c1 = min(c0 + kChunk, s1);
-            // the chunk's scales, a block a lane (32 of 16 slots at most); log2 for the values'
-            const int blk = (c0 >> rs) + lane;
-            const float ksl = blk < nb ? c.k_scale[(size_t)b * nb + blk] : 1.0f;
-            if (warp < nh) sm.lvs[warp][lane] = blk < nb ? __log2f(c.v_scale[(bh0 + warp) * nb + blk]) : 0.0f;
+            const float ksl = ks_next;
+            if (warp < nh) sm.lvs[warp][lane] = __log2f(vs_next);
+            if (c0 + kChunk < s1) fetch_scales(c0 + kChunk);
             __syncthreads();
             float cm[2] = {-INFINITY, -INFINITY}, cn[2] = {-3e38f, -3e38f};  // of heads 2 l4 and 2 l4 + 1
             // ---- scores
-            for (int t0 = c0 + 16 * warp; t0 < c1; t0 += 16 * kWarps) {
+            const int ke = min(c0 + kChunk, wend);
+            for (int t0 = c0 + 16 * warp; t0 < ke; t0 += 16 * kWarps) {
                 int lo, hi;
                 bounds(t0, lo, hi);
                 const float ks = __shfl_sync(0xffffffffu, ksl, (t0 - c0) >> rs);
@@ -554,13 +574,15 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
                 __syncwarp();
                 ask();
                 if (lo >= hi) continue;  // all of them in the tail
-                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains of products
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     const uint2 x = f16_pairs<I8>(ka[0][j]), y = f16_pairs<I8>(ka[1][j]);
                     const uint32_t a[4] = {x.x, y.x, x.y, y.y};
-                    mma_f16(s, a, qf[j][0], qf[j][1]);
+                    mma_f16(j & 1 ? s2 : s, a, qf[j][0], qf[j][1]);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] += s2[e];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int u = t0 + g + 8 * r;
@@ -730,6 +752,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
             __syncthreads();
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // key tiles that no position needed
     // ---- join the halves and parts, then the warps of a head
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
