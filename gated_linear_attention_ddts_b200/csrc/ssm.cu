@@ -478,13 +478,13 @@ int channels_per_block(int D, int N) {
 
 // Segments that a sequence is cut into: 1 where the channels alone give every SM
 // four blocks (the first launch repeats the exponentials), else enough for that,
-// each of at least four tiles.
+// each of at least two tiles.
 int segments(const SsmParams& p) {
     const long long blocks = (long long)p.B * p.H * (p.D / channels_per_block(p.D, p.N));
     const long long want = 4LL * sm_count();
     if (blocks * 2 > want) return 1;
     long long P = want / blocks;
-    const long long most = p.T / (4 * kTile);
+    const long long most = p.T / (2 * kTile);
     if (P > most) P = most;
     if (P > 64) P = 64;
     return P < 2 ? 1 : (int)P;

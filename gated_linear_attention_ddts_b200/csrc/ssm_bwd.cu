@@ -673,42 +673,43 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
     if (seg == 0 && bp.dS0) *reinterpret_cast<float4*>(bp.dS0 + srow) = g4;
 }
 
-// dB, dC: each group's rows of partial sums, in order.  One thread has four
-// neighbouring values of a row (dB and dC side by side).
+// The sums over blocks, sequences and segments, each in a fixed order, and the rows
+// where the convolution reaches over a segment's end.  First dB and dC: one thread
+// has four neighbouring values of a group's row (dB and dC side by side); then the
+// weights' gradients and the edges, one value a thread.
 template <typename T>
-__global__ void __launch_bounds__(256) ssm_bc_grad_kernel(const SsmBwdParams bp, const BwdWork wk) {
+__global__ void __launch_bounds__(256) ssm_finish_kernel(const SsmBwdParams bp, const BwdWork wk, const unsigned rowblocks) {
     const SsmParams& p = bp.f;
-    const int per = p.N / 2;  // float4 of a row
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (size_t)p.B * p.G * p.T * per) return;
-    const int n = (int)(i % per) * 4;
-    const size_t row = i / per;
-    const int t = (int)(row % p.T), bg = (int)(row / p.T), b = bg / p.G, g = bg % p.G;
-    const int hpg = p.H / p.G, rows = hpg * wk.nblk;
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (t < seq_len(p, b)) {
-        const float* part = wk.part + (((size_t)b * p.H + g * hpg) * wk.nblk * p.T + t) * 2 * p.N + n;
-        for (int k = 0; k < rows; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(part + (size_t)k * p.T * 2 * p.N);
-            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+    if (blockIdx.x < rowblocks) {
+        const int per = p.N / 2;  // float4 of a row
+        const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+        if (i >= (size_t)p.B * p.G * p.T * per) return;
+        const int n = (int)(i % per) * 4;
+        const size_t row = i / per;
+        const int t = (int)(row % p.T), bg = (int)(row / p.T), b = bg / p.G, g = bg % p.G;
+        const int hpg = p.H / p.G, rows = hpg * wk.nblk;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (t < seq_len(p, b)) {
+            const size_t step = (size_t)p.T * 2 * p.N;
+            const float* part = wk.part + (((size_t)b * p.H + g * hpg) * wk.nblk * p.T + t) * 2 * p.N + n;
+#pragma unroll 8
+            for (int k = 0; k < rows; ++k) {
+                const float4 v = *reinterpret_cast<const float4*>(part + k * step);
+                a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+            }
         }
+        T* out = static_cast<T*>(n < p.N ? bp.dB : bp.dC) + row * p.N + (n < p.N ? n : n - p.N);
+        stpair(out, a.x, a.y);
+        stpair(out + 2, a.z, a.w);
+        return;
     }
-    T* out = static_cast<T*>(n < p.N ? bp.dB : bp.dC) + row * p.N + (n < p.N ? n : n - p.N);
-    stpair(out, a.x, a.y);
-    stpair(out + 2, a.z, a.w);
-}
-
-// The weights' gradients over sequences and segments, in order, and the rows
-// where the convolution reaches over a segment's end.
-template <typename T>
-__global__ void __launch_bounds__(256) ssm_finish_kernel(const SsmBwdParams bp, const BwdWork wk) {
-    const SsmParams& p = bp.f;
     const size_t hd = (size_t)p.H * p.D, na = hd * p.N, np = hd * kPar;
     const size_t ne = wk.P > 1 && p.W > 1 ? (size_t)(wk.P - 1) * p.B * p.H * 3 * p.D : 0;
-    size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    size_t i = (size_t)(blockIdx.x - rowblocks) * 256 + threadIdx.x;
     const int parts = wk.P * p.B;
     if (i < na) {
         float a = 0.0f;
+#pragma unroll 8
         for (int k = 0; k < parts; ++k) a += wk.pA[k * na + i];
         bp.dA[i] = a;
         return;
@@ -719,6 +720,7 @@ __global__ void __launch_bounds__(256) ssm_finish_kernel(const SsmBwdParams bp, 
         float* out = k == 0 ? bp.ddt_bias : k == 1 ? bp.ddfeed : k == 2 ? bp.dcb : (k - 3 < p.W ? bp.dcw : nullptr);
         if (!out) return;
         float a = 0.0f;
+#pragma unroll 8
         for (int j = 0; j < parts; ++j) a += wk.pPar[j * np + i];
         out[k < 3 ? hc : (size_t)hc * p.W + k - 3] = a;
         return;
@@ -750,7 +752,7 @@ int segments(const SsmParams& p) {
     const long long want = 4LL * sm_count();
     if (blocks * 2 > want) return 1;
     long long P = want / blocks;
-    const long long most = p.T / (8 * kSsmChunk);
+    const long long most = p.T / (2 * kSsmChunk);
     if (P > most) P = most;
     if (P > 64) P = 64;
     return P < 2 ? 1 : (int)P;
@@ -823,14 +825,10 @@ cudaError_t launch_bwd_t(const SsmBwdParams& bp, const BwdWork& wk, cudaStream_t
         default: e = launch_bwd<T, 128, 8>(bp, wk, s); break;
     }
     if (e != cudaSuccess) return e;
-    const size_t rows = (size_t)p.B * p.G * p.T * (p.N / 2);
-    if (rows) {
-        ssm_bc_grad_kernel<T><<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(bp, wk);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
+    const unsigned rowblocks = (unsigned)(((size_t)p.B * p.G * p.T * (p.N / 2) + 255) / 256);
     const size_t hd = (size_t)p.H * p.D;
     const size_t n = hd * (p.N + kPar) + (wk.P > 1 && p.W > 1 ? (size_t)(wk.P - 1) * p.B * p.H * 3 * p.D : 0);
-    ssm_finish_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(bp, wk);
+    ssm_finish_kernel<T><<<rowblocks + (unsigned)((n + 255) / 256), 256, 0, s>>>(bp, wk, rowblocks);
     return cudaGetLastError();
 }
 
