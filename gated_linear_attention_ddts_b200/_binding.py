@@ -594,26 +594,20 @@ def _current(t, name) -> int:
 
 
 def _arg(t, name, shape, dtype, dev):
-    """The pointer of argument `name` after its checks; None is a null pointer."""
+    """The pointer of argument `name` after its checks; None is a null pointer
+    (which the library refuses where it needs one)."""
     if t is None:
         return 0
-    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == dev and \
-            t.is_contiguous():
-        return t.data_ptr()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name}: expected a torch.Tensor") from None
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     raise ValueError(f"{name}: tensors passed to the library must be contiguous and on cuda:{dev}")
-
-
-def _given(t, name, shape, dtype, dev):
-    """_arg for one that a call cannot do without."""
-    if t is None:
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    return _arg(t, name, shape, dtype, dev)
 
 
 def _buffer(t, dev):
@@ -632,17 +626,16 @@ def _code(t, name):
     return code
 
 
-def _width(conv_weight, *states):
-    """Taps of the convolution, 0 without one."""
+def _width(conv_weight, a=None, b=None, c=None):
+    """Taps of the convolution, 0 without one (and then none of its bias and states)."""
     if conv_weight is None:
-        W = 0
-    elif isinstance(conv_weight, torch.Tensor) and conv_weight.dim() == 3:
-        W = conv_weight.shape[-1]
-    else:
+        if a is None and b is None and c is None:
+            return 0
+    elif conv_weight.dim() != 3:
         raise ValueError("conv_weight: expected [H,D,W]")
-    if W == 0 and (conv_weight is not None or any(s is not None for s in states)):
-        raise ValueError("a convolution's bias or state needs conv_weight [H,D,W] with W >= 1")
-    return W
+    elif conv_weight.shape[2]:
+        return conv_weight.shape[2]
+    raise ValueError("a convolution's bias or state needs conv_weight [H,D,W] with W >= 1")
 
 
 def _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
@@ -656,7 +649,7 @@ def _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_b
     W = _width(conv_weight, conv_bias, conv_state_in, conv_state_out)
     seq, group, state, chan, cstate = (B, H, T, D), (B, G, T, N), (B, H, D, N), (H, D), (B, H, W - 1, D)
     return (B, H, G, T, D, N, W, _code(x, "x"), GATES[gates], 1 if conv_silu else 0, _arg(x, "x", seq, ty, dev),
-            _given(dt, "dt", seq, ty, dev), _arg(Bm, "Bm", group, ty, dev), _given(Cm, "Cm", group, ty, dev),
+            _arg(dt, "dt", seq, ty, dev), _arg(Bm, "Bm", group, ty, dev), _arg(Cm, "Cm", group, ty, dev),
             _arg(z, "z", seq, ty, dev), _arg(A, "A", (H, D, N), _F32, dev), _arg(dt_bias, "dt_bias", chan, _F32, dev),
             _arg(feedthrough, "feedthrough", chan, _F32, dev), _arg(conv_weight, "conv_weight", (H, D, W), _F32, dev),
             _arg(conv_bias, "conv_bias", chan, _F32, dev), _arg(conv_state_in, "conv_state_in", cstate, ty, dev),
@@ -727,7 +720,7 @@ def _ssm_bwd_args(a, grad_y, grad_ST, grad_conv_state_out, g, ty, dev):
     """The fields of rdm_ssm_bwd_args behind the forward's."""
     B, H, G, T, D, N, W = a[:7]
     seq, state, group, chan, cstate = (B, H, T, D), (B, H, D, N), (B, G, T, N), (H, D), (B, H, W - 1, D)
-    return (_given(grad_y, "grad_y", seq, ty, dev), _arg(grad_ST, "grad_ST", state, _F32, dev),
+    return (_arg(grad_y, "grad_y", seq, ty, dev), _arg(grad_ST, "grad_ST", state, _F32, dev),
             _arg(grad_conv_state_out, "grad_conv_state_out", cstate, ty, dev), _arg(g["dx"], "dx", seq, ty, dev),
             _arg(g["ddt"], "ddt", seq, ty, dev), _arg(g["dz"], "dz", seq, ty, dev), _arg(g["dB"], "dB", group, ty, dev),
             _arg(g["dC"], "dC", group, ty, dev), _arg(g["dA"], "dA", (H, D, N), _F32, dev),
@@ -800,10 +793,10 @@ def rdm_ssm_step(x, dt, A, Bm, Cm, S, *, z=None, dt_bias=None, feedthrough=None,
         y = torch.empty_like(x)
     _launch("rdm_ssm_step", _SSM_STEP.pack(
         B, H, G, D, N, W, _code(x, "x"), GATES[gates], 1 if conv_silu else 0, _arg(x, "x", seq, ty, dev),
-        _given(dt, "dt", seq, ty, dev), _arg(Bm, "Bm", (B, G, N), ty, dev), _given(Cm, "Cm", (B, G, N), ty, dev),
+        _arg(dt, "dt", seq, ty, dev), _arg(Bm, "Bm", (B, G, N), ty, dev), _arg(Cm, "Cm", (B, G, N), ty, dev),
         _arg(z, "z", seq, ty, dev), _arg(A, "A", (H, D, N), _F32, dev), _arg(dt_bias, "dt_bias", chan, _F32, dev),
         _arg(feedthrough, "feedthrough", chan, _F32, dev), _arg(conv_weight, "conv_weight", (H, D, W), _F32, dev),
-        _arg(conv_bias, "conv_bias", chan, _F32, dev), _given(S, "S", (B, H, D, N), _F32, dev),
+        _arg(conv_bias, "conv_bias", chan, _F32, dev), _arg(S, "S", (B, H, D, N), _F32, dev),
         _arg(conv_state, "conv_state", (B, H, W - 1, D), ty, dev) if W > 1 else 0, _arg(y, "y", seq, ty, dev)), dev)
     return y
 
@@ -838,9 +831,9 @@ def _q8_cache(B, H, dk, dv, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, 
     w, R = k_cache.shape[1], k_tail.shape[1]
     nb = (w + R - 1) // R
     return (B, H, dk, dv, w, R, kind, _arg(k_cache, "k_cache", (B, w, dk), ty, dev),
-            _given(v_cache, "v_cache", (B, H, w, dv), ty, dev), _given(k_scale, "k_scale", (B, nb), _F32, dev),
-            _given(v_scale, "v_scale", (B, H, nb), _F32, dev), _arg(k_tail, "k_tail", (B, R, dk), _BF16, dev),
-            _given(v_tail, "v_tail", (B, H, R, dv), _BF16, dev), _given(pos, "pos", (B,), _I32, dev))
+            _arg(v_cache, "v_cache", (B, H, w, dv), ty, dev), _arg(k_scale, "k_scale", (B, nb), _F32, dev),
+            _arg(v_scale, "v_scale", (B, H, nb), _F32, dev), _arg(k_tail, "k_tail", (B, R, dk), _BF16, dev),
+            _arg(v_tail, "v_tail", (B, H, R, dv), _BF16, dev), _arg(pos, "pos", (B,), _I32, dev))
 
 
 def rdm_ska_q8_fill(k, v, k_cache, v_cache, k_scale, v_scale, k_tail, v_tail, pos, *, lengths=None, stream=None):
@@ -870,7 +863,7 @@ def _q8_decode_args(q, k, v, cache, scale, o, advance_pos):
     B, H, dk = q.shape
     dv, ty = v.shape[2], q.dtype
     return (*_q8_cache(B, H, dk, dv, *cache, dev), float(scale), _code(q, "q"), _arg(q, "q", (B, H, dk), ty, dev),
-            _given(k, "k", (B, dk), ty, dev), _arg(v, "v", (B, H, dv), ty, dev), _arg(o, "o", (B, H, dv), ty, dev),
+            _arg(k, "k", (B, dk), ty, dev), _arg(v, "v", (B, H, dv), ty, dev), _arg(o, "o", (B, H, dv), ty, dev),
             1 if advance_pos else 0), dev
 
 
