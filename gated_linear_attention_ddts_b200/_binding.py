@@ -700,16 +700,16 @@ def rdm_ssm_fwd(x, dt, A, Bm, Cm, *, S0=None, z=None, dt_bias=None, feedthrough=
     if return_state:
         B, H, _, D = x.shape
         if ST is None:
-            ST = torch.empty((B, H, D, A.shape[-1]), dtype=_F32, device=x.device)
+            ST = A.new_empty((B, H, D, A.shape[-1]))
         if conv_state_out is None and conv_weight is not None:
-            conv_state_out = torch.empty((B, H, conv_weight.shape[-1] - 1, D), dtype=x.dtype, device=x.device)
+            conv_state_out = x.new_empty((B, H, conv_weight.shape[-1] - 1, D))
     a, dev = _ssm_args(x, dt, A, Bm, Cm, S0, z, dt_bias, feedthrough, conv_weight, conv_bias, conv_state_in,
                        conv_silu, lengths, gates, y, ST, conv_state_out, saved_states)
     packed = _SSM.pack(*a, 0, 0)
     if workspace is None:
         need = _size("rdm_ssm_fwd", packed)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = x.new_empty(need, dtype=torch.uint8)
     if workspace is not None and workspace is not False:
         packed = _SSM.pack(*a, *_buffer(workspace, dev))
     _launch("rdm_ssm_fwd", packed, dev)
@@ -765,7 +765,7 @@ def rdm_ssm_bwd(x, dt, A, Bm, Cm, grad_y, grad_ST=None, grad_conv_state_out=None
         need = _size("rdm_ssm_bwd", _SSM_BWD.pack(*a, 0, 0, *b))
         ws = (0, 0)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = x.new_empty(need, dtype=torch.uint8)
     if workspace is not None:
         ws = _buffer(workspace, dev)
     _launch("rdm_ssm_bwd", _SSM_BWD.pack(*a, *ws, *b), dev)
@@ -888,7 +888,7 @@ def rdm_ska_q8_decode(q, k, v, k_cache, v_cache, k_scale, v_scale, k_tail, v_tai
     if workspace is None:
         need = _size("rdm_ska_q8_decode", packed)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(need, dtype=torch.uint8)
     if workspace is not None and workspace is not False:
         packed = _Q8_DECODE.pack(*a, *_buffer(workspace, dev))
     _launch("rdm_ska_q8_decode", packed, dev)

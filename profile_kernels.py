@@ -1,7 +1,8 @@
 #!/usr/bin/env python
 """Small launches of each kernel, the command that profiler captures wrap.
 
-    python profile_kernels.py fwd1|fwd1pre|fwd1feed|fwd1lr|fwd2|fwdbwd3|bwdwide3|decode4|conv1|ska1|ska4
+    python profile_kernels.py fwd1|fwd1pre|fwd1feed|fwd1lr|fwd2|fwdbwd3|bwdwide3|decode4|conv1|ska1|ska4|
+                              ssm1|ssmbwd1|ssmstep|q8fill|q8dec
 
 One workload per call: the mode draws its inputs on the device, runs the
 kernel(s) three times and synchronises.  fwd1 is the 130M-scale layer forward
@@ -17,7 +18,11 @@ layer with the gates passed before their activations and a rank-16 beta_hat, con
 ShortConv forward and backward (width 4, SiLU) on a q-shaped tensor of that
 layer (B8 H6 T2048 D64), ska1 the sliding-window shared-key attention forward
 (B8 H12 T2048 d_k=d_v=64, window 512) and ska4 its batched decode step against
-full ring caches (B256 H16 d_k=d_v=128, window 512).
+full ring caches (B256 H16 d_k=d_v=128, window 512); ssm1 the selective scan
+forward (B8 H24 T512 D64 N16, width-4 convolution, gate), ssmbwd1 its forward with
+saved states and backward (B4), ssmstep one token of it (B256 H16 D128 N64), q8fill
+four prompts into 8-bit rings (H16 T16384 d128, 8200 slots in blocks of 16, int8) and
+q8dec the decode step of ska4 over 8-bit rings (e4m3, blocks of 64).
 Exit status 0 only when the library's device status word is clear."""
 import os
 import sys
@@ -73,6 +78,41 @@ def main(mode: str) -> int:
             pos = torch.full((B,), 1000, dtype=torch.int32, device="cuda")
             for _ in range(3):
                 rdm.rdm_ska_decode(q, k, v, kc, vc, pos)
+    elif mode in ("ssm1", "ssmbwd1", "ssmstep"):
+        step = mode == "ssmstep"
+        B, H, T, D, N = {"ssm1": (8, 24, (512,), 64, 16), "ssmbwd1": (4, 24, (512,), 64, 16),
+                         "ssmstep": (256, 16, (), 128, 64)}[mode]
+        bf = dict(device="cuda", dtype=torch.bfloat16)
+        x, dt, z = torch.randn(B, H, *T, D, **bf), torch.randn(B, H, *T, D, **bf), torch.randn(B, H, *T, D, **bf)
+        Bm, Cm = torch.randn(B, 1, *T, N, **bf), torch.randn(B, 1, *T, N, **bf)
+        A = -torch.arange(1.0, N + 1, device="cuda").expand(H, D, N).contiguous()
+        given = dict(z=z, dt_bias=torch.full((H, D), -4.0, device="cuda"), feedthrough=torch.ones(H, D, device="cuda"),
+                     conv_weight=torch.randn(H, D, 4, device="cuda") / 2, conv_bias=torch.zeros(H, D, device="cuda"))
+        if step:
+            S, cs = torch.zeros(B, H, D, N, device="cuda"), torch.zeros(B, H, 3, D, **bf)
+        saved = rdm.rdm_ssm_saved_states(x, A) if mode == "ssmbwd1" else None
+        for _ in range(3):
+            if step:
+                rdm.rdm_ssm_step(x, dt, A, Bm, Cm, S, conv_state=cs, **given)
+                continue
+            y, _, _ = rdm.rdm_ssm_fwd(x, dt, A, Bm, Cm, saved_states=saved, **given)
+            if saved is not None:
+                rdm.rdm_ssm_bwd(x, dt, A, Bm, Cm, y, saved_states=saved, **given)
+    elif mode in ("q8fill", "q8dec"):
+        bf = dict(device="cuda", dtype=torch.bfloat16)
+        if mode == "q8fill":
+            cache = rdm.rdm_ska_q8_cache(4, 16, 128, 128, 8200, block=16, dtype=torch.int8)
+            k, v = torch.randn(4, 16384, 128, **bf), torch.randn(4, 16, 16384, 128, **bf)
+            for _ in range(3):
+                rdm.rdm_ska_q8_fill(k, v, *cache)
+        else:
+            B, H, d, win, _ = SKA_DEC
+            cache = rdm.rdm_ska_q8_cache(B, H, d, d, win)
+            rdm.rdm_ska_q8_fill(torch.randn(B, win, d, **bf), torch.randn(B, H, win, d, **bf), *cache)
+            q, k, v = torch.randn(B, H, d, **bf), torch.randn(B, d, **bf), torch.randn(B, H, d, **bf)
+            cache[6].copy_(1000 + 37 * torch.arange(B, device="cuda"))
+            for _ in range(3):
+                rdm.rdm_ska_q8_decode(q, k, v, *cache)
     elif mode in ("fwdbwd3", "bwdwide3"):
         w = WORKLOADS[3]
         x = draw_workload(w, device="cuda")
