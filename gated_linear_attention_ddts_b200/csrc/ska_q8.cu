@@ -262,13 +262,18 @@ __global__ void __launch_bounds__(kThreads) ska_q8_fill_kernel(const SkaQ8FillPa
 //           into f16 pairs in registers (exact: e4m3 and int8 both fit f16's 11 bits)
 // Without the tensor cores the conversions and products of the values alone would
 // cost about 70 of an SM's 128 lane operations a clock at the memory's rate; with
-// them each byte of V costs 0.25 byte permutations, half a conversion and 1/256 of
-// an mma a warp, and the sweep stays bound by HBM.
+// them each byte of V costs a quarter of a byte permutation, half a conversion and
+// 1/256 of an mma a warp.  (Tried: mma on the codes themselves, e4m3 or int8, the
+// weights in four parts of that type: right to 2^-24, but more instructions in all,
+// 103 us against 85 at B256 H16 d128 window 512.)
 // The tail's slots go through the same steps in bf16, the weights in three parts.
 // Each warp's tiles (the keys', then the values' of its head) come through a ring
-// of its own, four tiles ahead, so that 64 KB a CTA are on their way in every phase;
-// with loads into registers two tiles ahead and nothing in flight between the
-// phases HBM ran at 37% (B256 H16 d128 window 512: 106 us against XXX).
+// of its own, four tiles ahead (two or five measure the same).  Bound: the phases
+// before and behind the sweep of V, in which little is on its way: a kernel that only
+// streams the same V through the same rings takes 45 us, this one 83 (3.7 TB/s), of
+// which the tail's rows cost 13; the bf16 rings' kernel (ska.cu) takes 119 for 1.9
+// times the bytes.  One sequence, window 32768: 27 us, a second kernel joining 128
+// splits included.
 constexpr int kWarps = 8, kDecThreads = 32 * kWarps, kChunk = 512, kStride = kChunk + 4, kRing = 4;
 
 template <int DK, int DV>

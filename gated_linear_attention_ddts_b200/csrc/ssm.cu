@@ -10,7 +10,9 @@
 //
 // The decays differ by channel and state, so there is no matrix product in it:
 // the recurrence runs on the CUDA cores in float32, and its floor is the
-// exponential unit (one ex2 per channel, token and state; 16 a clock and SM).
+// exponential unit (one ex2 per channel, token and state; 16 a clock and SM): 61 us
+// for B8 H24 D64 N16 of ragged T up to 2048 (11608 tokens), 84 with the six of delta,
+// u and the gate; it takes 164, HBM would take 22.
 //
 // Forward: a block has CPB channels of one (b, h), four states a thread, and
 // walks its tokens in tiles of 32.  Threads first make delta and u of the tile

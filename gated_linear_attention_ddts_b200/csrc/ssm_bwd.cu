@@ -9,16 +9,19 @@
 //   dzc = du silu'(zc)        dx_t = sum_i w_i dzc_{t+i}     dw_i = sum_t dzc_t x_{t-i}
 //
 // A block has CPB channels of one (b, h), four states a thread, and walks its
-// chunks of 16 tokens backwards.  From the state saved before a chunk it runs
-// the recurrence forward again, keeping all 16 states of the chunk in registers
-// (64 of them), then backwards; sums over n are shuffles within a channel's
-// lanes for four tokens at a time, sums over channels (dB, dC) a transposing
-// reduction over the warp's channels, then shared memory over the block's warps,
-// then one row of partial sums per block that a last kernel adds up in a fixed
-// order: no atomics, so the same call gives the same bits.  Sequences are cut
-// into segments as in the forward; a first launch then runs G alone over each
-// segment but the first from zero, and each block folds the segments behind its
+// chunks of 16 tokens backwards.  From the state saved before a chunk it runs the
+// recurrence forward again, keeps the states before each four tokens, then takes
+// the fours backwards, their own states and decays in registers.  Sums over n are
+// shuffles within a channel's lanes for four tokens at a time, sums over channels
+// (dB, dC) a transposing reduction over the warp's channels, then shared memory over
+// the block's warps, then one row of partial sums per block that a last kernel adds
+// up in a fixed order: no atomics, so the same call gives the same bits.  Sequences
+// are cut into segments as in the forward; a first launch then runs G alone over
+// each segment but the first from zero, and each block folds the segments behind its
 // own.  The convolution's reach over a segment's end is added by the last kernel.
+// Bound: instructions (147 a warp, token and 128 states, 54% of the issue slots) and
+// the shared-memory pipe (40%); the exponentials, the floor, are 26%.  B4 H24 T2048
+// D64 N16 bf16: forward and backward 581 us, 410 of them this kernel.
 #include "launch.h"
 #include "ssm_common.cuh"
 
@@ -532,9 +535,8 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
         }
         // First the states before each four tokens (kept, 12 registers), then for each
         // four tokens, the last first, their states forward (16 registers) and back.
-        // (With all sixteen states kept the code of a chunk outgrew the instruction
-        // cache and 168 registers left two blocks an SM: 430 us against 370 of the
-        // training step.)
+        // (With all sixteen states kept, and every decay evaluated twice, the code of
+        // a chunk outgrew the instruction cache: 642 us against 586 a training step.)
         float2 before[kQuads][2];
         before[0][0] = make_float2(next_state.x, next_state.y);
         before[0][1] = make_float2(next_state.z, next_state.w);

@@ -100,6 +100,17 @@ def test_heads_and_positions(cuda_ok, kind, H):
     ref.assert_state(cache, caches, "after the last token")
 
 
+@pytest.mark.parametrize("H", [65, 67, 72])
+def test_more_heads_than_a_cluster(cuda_ok, H):
+    """More than eight groups of heads: the positions are advanced by a kernel of
+    their own."""
+    q, k, v = tokens(2, H, 70, 64, 64, seed=H)
+    cache, caches = filled(k[:, :60], v[:, :, :60], 48, 16, torch.int8, [60, 31])
+    for t in range(60, 64):
+        step(q[:, :, t], k[:, t], v[:, :, t], cache, caches, what=f"token {t}")
+    ref.assert_state(cache, caches, "after the last token")
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("B,H,window,block,T", [(1, 4, 5000, 64, 5203), (2, 1, 3001, 16, 2900), (1, 16, 1500, 32, 1490), (1, 9, 2048, 64, 2048)])
 def test_long_windows(cuda_ok, kind, B, H, window, block, T):
@@ -247,6 +258,23 @@ def test_graph_replayed_token_by_token(cuda_ok, B, H, window):
         want = torch.stack([c.attend(q[b, :, t], c.add(k[b, t], v[b, :, t]), 1 / 8) for b, c in enumerate(caches)])
         ref.assert_out(o, want, largest, f"token {t}")
     ref.assert_state(cache, caches, "after the last token")
+
+
+def test_two_streams_at_once(cuda_ok):
+    """Two caches decoded on two streams, split windows with a workspace each, equal
+    the same calls one after the other."""
+    q, k, v = tokens(2, 4, 2100, 64, 64, seed=30)
+    made = [filled(k[b:b + 1, :2090].contiguous(), v[b:b + 1, :, :2090].contiguous(), 2050, 32, torch.int8)[0] for b in range(2)]
+    args = [[t[b:b + 1].contiguous().cuda() for t in (q[:, :, 2090], k[:, 2090], v[:, :, 2090])] for b in range(2)]
+    want = [rdm.rdm_ska_q8_decode(*a, *c, advance_pos=False).clone() for a, c in zip(args, made)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for b in range(2):
+            got[b].append(rdm.rdm_ska_q8_decode(*args[b], *made[b], advance_pos=False, stream=streams[b]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[b]) for b in range(2) for o in got[b])
 
 
 def test_same_bits_every_time(cuda_ok):

@@ -246,6 +246,22 @@ def test_same_bits_every_time(cuda_ok):
         assert all(torch.equal(first[n], again[n]) for n in first)
 
 
+def test_two_streams_at_once(cuda_ok):
+    """Two training steps of cut sequences on two streams equal the same calls one
+    after the other."""
+    ds = [cuda(ref.inputs(1, 2, 700, 32, 16, seed=50 + k, dtype=BF16)) for k in range(2)]
+    gys = [torch.randn_like(d["x"]) for d in ds]
+    want = [call(rdm.rdm_ssm_bwd, d, gy) for d, gy in zip(ds, gys)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for k in range(2):
+            got[k].append(call(rdm.rdm_ssm_bwd, ds[k], gys[k], stream=streams[k]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g[n], want[k][n]) for k in range(2) for g in got[k] for n in g)
+
+
 def test_other_stream_and_graph(cuda_ok):
     """A call on a side stream, and a captured prompt and token replayed with
     new inputs in the same buffers."""
