@@ -65,7 +65,7 @@ struct FwdSmem {
 // one kind doing all three in turn only 58% of the issue slots were used (2.6
 // warps a scheduler at B8 H24 D64, each waiting for itself): 190 us against 165.
 template <typename T, int N, int CPB, bool LOCAL>
-__global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 2 : 3)
+__global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 2 : CPB * N / 4 > 64 ? 3 : 5)
     ssm_fwd_kernel(const SsmParams p, const SegArgs sg) {
     using L = Lay<N, CPB>;
     constexpr int LPC = L::LPC, TH = L::THREADS, EW = kEw<CPB>, UNITS = (kTile / 4) * (CPB / 2);
@@ -473,23 +473,34 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmStepPar
     }
 }
 
-int channels_per_block(int D, int N) {
-    const int most = N == 16 ? 32 : N == 32 ? 16 : 8;
-    return D < most ? D : most;
-}
-
-// Segments that a sequence is cut into: 1 where the channels alone give every SM
-// four blocks (the first launch repeats the exponentials), else enough for that,
-// each of at least two tiles.
-int segments(const SsmParams& p) {
-    const long long blocks = (long long)p.B * p.H * (p.D / channels_per_block(p.D, p.N));
-    const long long want = 4LL * sm_count();
-    if (blocks * 2 > want) return 1;
-    long long P = want / blocks;
+// Channels a block and segments a sequence.  Measured at H24 D64 N16 bf16, 8192
+// tokens in all (us, P = 1 against the best P):
+//   B1 (48 blocks of 32 channels) 410 / 172 (P = 24)   B2 (96) 209 / 165 (P = 16)
+//   B4 (192) 152 / 156 (P = 3)
+// so sequences stay whole where the blocks reach the number of SMs (the first
+// launch of a cut scan repeats nearly all of the work), and else are cut for six
+// blocks an SM, each segment of at least two tiles.  Whole sequences of at most two
+// blocks an SM run 16 channels a block (B4: 132 us); with more, 32 is faster
+// (B8 T2048: 213 against 245).
+struct Cut {
+    int cpb, P;
+};
+Cut cut(const SsmParams& p) {
+    Cut c;
+    c.cpb = p.N == 16 ? 32 : p.N == 32 ? 16 : 8;
+    if (c.cpb > p.D) c.cpb = p.D;
+    const long long blocks = (long long)p.B * p.H * (p.D / c.cpb), sms = sm_count();
+    c.P = 1;
+    if (blocks >= sms) {
+        if (p.N == 16 && blocks < 2 * sms) c.cpb = 16;
+        return c;
+    }
+    long long P = 6 * sms / blocks;
     const long long most = p.T / (2 * kTile);
     if (P > most) P = most;
     if (P > 64) P = 64;
-    return P < 2 ? 1 : (int)P;
+    c.P = P < 2 ? 1 : (int)P;
+    return c;
 }
 int segment_len(int T, int P) {
     const int tiles = (T + kTile - 1) / kTile;
@@ -519,9 +530,9 @@ cudaError_t launch_fwd(const SsmParams& p, const SegArgs& sg, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_fwd_t(const SsmParams& p, const SegArgs& sg, cudaStream_t s) {
+cudaError_t launch_fwd_t(const SsmParams& p, const SegArgs& sg, int cpb, cudaStream_t s) {
     switch (p.N) {
-        case 16: return p.D >= 32 ? launch_fwd<T, 16, 32>(p, sg, s) : launch_fwd<T, 16, 16>(p, sg, s);
+        case 16: return cpb == 32 ? launch_fwd<T, 16, 32>(p, sg, s) : launch_fwd<T, 16, 16>(p, sg, s);
         case 32: return launch_fwd<T, 32, 16>(p, sg, s);
         case 64: return launch_fwd<T, 64, 8>(p, sg, s);
         default: return launch_fwd<T, 128, 8>(p, sg, s);
@@ -555,17 +566,18 @@ cudaError_t launch_step_t(const SsmStepParams& p, cudaStream_t s) {
 }  // namespace
 
 size_t ssm_fwd_workspace(const SsmParams& p) {
-    const int P = segments(p);
+    const int P = cut(p).P;
     return P < 2 ? 0 : (size_t)(P - 1) * p.B * p.H * p.D * (p.N + 1) * 4;
 }
 
 cudaError_t launch_ssm_fwd(const SsmParams& p, cudaStream_t s) {
     SegArgs sg;
-    sg.P = p.ws && p.ws_bytes >= ssm_fwd_workspace(p) ? segments(p) : 1;
+    const Cut c = cut(p);
+    sg.P = p.ws && p.ws_bytes >= ssm_fwd_workspace(p) ? c.P : 1;
     sg.len = segment_len(p.T, sg.P);
     sg.local = static_cast<float*>(p.ws);
     sg.dsum = sg.local + (size_t)(sg.P - 1) * p.B * p.H * p.D * p.N;
-    return p.bf16 ? launch_fwd_t<__nv_bfloat16>(p, sg, s) : launch_fwd_t<float>(p, sg, s);
+    return p.bf16 ? launch_fwd_t<__nv_bfloat16>(p, sg, c.cpb, s) : launch_fwd_t<float>(p, sg, c.cpb, s);
 }
 
 cudaError_t launch_ssm_step(const SsmStepParams& p, cudaStream_t s) {
