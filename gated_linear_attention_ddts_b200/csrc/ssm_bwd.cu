@@ -21,7 +21,8 @@
 // own.  The convolution's reach over a segment's end is added by the last kernel.
 // Bound: instructions (147 a warp, token and 128 states, 54% of the issue slots) and
 // the shared-memory pipe (40%); the exponentials, the floor, are 26%.  B4 H24 T2048
-// D64 N16 bf16: forward and backward 581 us, 410 of them this kernel.
+// D64 N16 bf16: forward and backward 560 us, 361 of them this kernel
+// and 68 its first launch.
 #include "launch.h"
 #include "ssm_common.cuh"
 
@@ -749,15 +750,28 @@ int channels_per_block(int D, int N) {
     return D < most ? D : most;
 }
 
+// Segments a sequence: the count of least cost, where two blocks an SM run at a time, a
+// segment costs its tokens and a chunk to start and end, and the first launch for the
+// states is a tenth of the work of all segments but one; each of at least two chunks.
+// Measured, a training step with D64 N16 bf16 (us, whole sequences / this rule's P):
+// B1 H24 T4096 871 / 324 (6), B2 H24 T4096 958 / 625 (3), B4 H24 T2048 664 / 563 (3),
+// B1 H3 T4096 787 / 73 (49), B1 H4 T512 113 / 31 (16), B3 H20 T2048 505 / 388 (7); it
+// keeps P = 1 at B16 H24 T512, 514 against 549 of P = 3, and at B32 H24 T128, 268
+// against 336.  At B5 H24 T777 it loses: 301 (6) against 278.
 int segments(const SsmParams& p) {
-    const long long blocks = (long long)p.B * p.H * (p.D / channels_per_block(p.D, p.N));
-    const long long want = 4LL * sm_count();
-    if (blocks * 2 > want) return 1;
-    long long P = want / blocks;
-    const long long most = p.T / (2 * kSsmChunk);
-    if (P > most) P = most;
-    if (P > 64) P = 64;
-    return P < 2 ? 1 : (int)P;
+    const long long blocks = (long long)p.B * p.H * (p.D / channels_per_block(p.D, p.N)), round = 2LL * sm_count();
+    const int most = p.T / (2 * kSsmChunk) < 64 ? p.T / (2 * kSsmChunk) : 64;
+    int best = 1;
+    double least = 0;
+    for (int P = 1; P == 1 || P <= most; ++P) {
+        const long long rounds = (blocks * P + round - 1) / round;
+        const double cost = rounds * ((double)p.T / P + kSsmChunk) * (1.0 + 0.1 * (P - 1) / P);
+        if (P == 1 || cost < least) {
+            least = cost;
+            best = P;
+        }
+    }
+    return best;
 }
 
 size_t up(size_t n) { return (n + 63) / 64 * 64; }  // floats, so that each part starts on 256 bytes
