@@ -545,8 +545,9 @@ static rdm_status ssm_check(const rdm_ssm_args* a) {
         return RDM_ERR_INVALID_ARG;
     if ((a->dtype != RDM_F32 && a->dtype != RDM_BF16) || !gates_ok(a->gate_inputs)) return RDM_ERR_INVALID_ARG;
     if (!ssm_dim_ok(a->D) || !ssm_dim_ok(a->N) || a->W > 4) return RDM_ERR_UNSUPPORTED;
-    // blocks of eight channels or more fit a grid, element offsets 63 bits
-    if ((double)a->B * a->H * a->D > 8.0e9 || a->T > (1 << 30)) return RDM_ERR_INVALID_ARG;
+    // blocks of eight channels or more fit a grid, a channel's index 31 bits, element offsets 63
+    if ((double)a->B * a->H * a->D > 8.0e9 || (double)a->H * a->D > 2147483647.0 || a->T > (1 << 30))
+        return RDM_ERR_INVALID_ARG;
     if (!a->A || !aligned(a->A) || (a->W > 0) != (a->conv_weight != nullptr)) return RDM_ERR_INVALID_ARG;
     if (a->T > 0) {
         const void* in[] = {a->x, a->dt, a->Bm, a->Cm};
@@ -599,6 +600,10 @@ rdm_status rdm_ssm_fwd(const rdm_ssm_args* a, rdm_stream_t stream) {
     if ((a->T > 0 && !a->y) || !opt_aligned(a->y) || !opt_aligned(a->ST) || !opt_aligned(a->conv_state_out))
         return RDM_ERR_INVALID_ARG;
     if (a->W == 0 && a->conv_state_out) return RDM_ERR_INVALID_ARG;
+    // in place: other blocks still read what a block writes
+    if (a->y && (a->y == a->x || a->y == a->dt || a->y == a->z)) return RDM_ERR_INVALID_ARG;
+    if ((a->ST && a->ST == a->S0) || (a->conv_state_out && a->conv_state_out == a->conv_state_in))
+        return RDM_ERR_INVALID_ARG;
     SsmParams p = ssm_params(a);
     p.err = status_word();
     if (!p.err) return RDM_ERR_CUDA;
@@ -647,6 +652,9 @@ rdm_status rdm_ssm_bwd(const rdm_ssm_bwd_args* a, rdm_stream_t stream) {
     if ((a->grad_dt_bias && f.gate_inputs != RDM_GATES_PREACT) || (a->grad_feedthrough && !f.feedthrough) ||
         (f.W == 0 && (a->grad_conv_weight || a->grad_conv_bias || a->grad_conv_state_in || a->grad_conv_state_out)))
         return RDM_ERR_INVALID_ARG;
+    if ((a->grad_S0 && a->grad_S0 == a->grad_ST) ||
+        (a->grad_conv_state_in && a->grad_conv_state_in == a->grad_conv_state_out))
+        return RDM_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     SsmBwdParams p = ssm_bwd_params(a);
     if (f.T == 0) {  // no tokens: the carried gradients pass through, the weights have none
@@ -674,7 +682,7 @@ rdm_status rdm_ssm_step(const rdm_ssm_step_args* a, rdm_stream_t stream) {
     if (!a || a->B < 1 || a->H < 1 || a->G < 1 || a->W < 0 || a->H % a->G != 0) return RDM_ERR_INVALID_ARG;
     if ((a->dtype != RDM_F32 && a->dtype != RDM_BF16) || !gates_ok(a->gate_inputs)) return RDM_ERR_INVALID_ARG;
     if (!ssm_dim_ok(a->D) || !ssm_dim_ok(a->N) || a->W > 4) return RDM_ERR_UNSUPPORTED;
-    if ((double)a->B * a->H * a->D > 8.0e9) return RDM_ERR_INVALID_ARG;
+    if ((double)a->B * a->H * a->D > 8.0e9 || (double)a->H * a->D > 2147483647.0) return RDM_ERR_INVALID_ARG;
     const void* in[] = {a->x, a->dt, a->Bm, a->Cm, a->A, a->S, a->y};
     for (const void* p : in)
         if (!p || !aligned(p)) return RDM_ERR_INVALID_ARG;

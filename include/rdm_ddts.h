@@ -511,7 +511,7 @@ size_t rdm_ska_q8_decode_workspace_size(const rdm_ska_q8_decode_args *args);
  *   x, dt, y      : [B,H,T,D] dtype        D in {16, 32, 64, 128}
  *   Bm, Cm        : [B,G,T,N] dtype        N in {16, 32, 64, 128}; G divides H
  *   z             : [B,H,T,D] dtype gate, or NULL for none
- *   A             : [H,D,N] float32 (negative for a decay; not checked)
+ *   A             : [H,D,N] float32, finite (negative for a decay; not checked)
  *   dt_bias       : [H,D] float32 or NULL (zero); PREACT only
  *   feedthrough   : [H,D] float32 or NULL (none)
  *   conv_weight   : [H,D,W] float32, W <= 4, NULL exactly when W = 0
@@ -535,7 +535,8 @@ size_t rdm_ska_q8_decode_workspace_size(const rdm_ska_q8_decode_args *args);
  *                   run side by side.  Contents on entry are ignored; calls
  *                   whose kernels may overlap must not share it.
  * Arithmetic is float32 throughout, on either dtype.  Outputs must not alias
- * inputs.  The result of a call is the same bits every time. */
+ * inputs (y, ST and conv_state_out at the address of an input are refused).  The
+ * result of a call is the same bits every time. */
 typedef struct {
     int B, H, G, T, D, N, W;
     rdm_dtype dtype;
@@ -616,6 +617,7 @@ rdm_status rdm_ssm_step(const rdm_ssm_step_args *args, rdm_stream_t stream);
 
 /* Synchronises `stream`, then reports (and clears) the device status word of
  * the current device: RDM_ERR_TIMEOUT if a bounded wait in a kernel ran out,
+ * RDM_ERR_INVALID_ARG if a kernel met a position or length out of range,
  * RDM_ERR_CUDA if the stream holds a CUDA error, RDM_OK otherwise. */
 rdm_status rdm_ddts_sync_status(rdm_stream_t stream);
 

@@ -99,6 +99,30 @@ def test_step_refusals(lib, kw, status):
     assert lib.rdm_ssm_step(ctypes.byref(_binding.SsmStepArgs(**{**base, **kw})), None) == status
 
 
+@pytest.mark.parametrize("kw", [
+    dict(S0=FAKE + 64, ST=FAKE + 64), dict(y=FAKE), dict(z=FAKE + 64, y=FAKE + 64), dict(x=FAKE + 64, y=FAKE + 64),
+    dict(W=2, conv_weight=FAKE, conv_state_in=FAKE + 64, conv_state_out=FAKE + 64)])
+def test_fwd_refuses_outputs_in_place(lib, kw):
+    """Segments read the carried state while the last one writes the new one."""
+    assert lib.rdm_ssm_fwd(ctypes.byref(fwd_args(**{"y": FAKE + 128, **kw})), None) == 1
+
+
+@pytest.mark.parametrize("kw", [
+    dict(grad_ST=FAKE, grad_S0=FAKE), dict(grad_conv_state_in=FAKE, grad_conv_state_out=FAKE)])
+def test_bwd_refuses_outputs_in_place(lib, kw):
+    base = dict(grad_y=FAKE, grad_x=FAKE, grad_dt=FAKE, grad_B=FAKE, grad_C=FAKE, grad_A=FAKE)
+    a = _binding.SsmBwdArgs(fwd_args(W=2, conv_weight=FAKE), **{**base, **kw})
+    assert lib.rdm_ssm_bwd(ctypes.byref(a), None) == 1
+
+
+def test_refuses_more_channels_than_an_index_holds(lib):
+    a = fwd_args(B=1, H=1 << 25, G=1, T=1, y=FAKE + 128)
+    assert lib.rdm_ssm_fwd(ctypes.byref(a), None) == 1
+    s = _binding.SsmStepArgs(B=1, H=1 << 25, G=1, D=64, N=16, W=0, dtype=1, gate_inputs=1, conv_silu=1, x=FAKE, dt=FAKE,
+                             Bm=FAKE, Cm=FAKE, A=FAKE, S=FAKE, y=FAKE)
+    assert lib.rdm_ssm_step(ctypes.byref(s), None) == 1
+
+
 def test_sizes(lib):
     assert rdm.rdm_ssm_saved_states_size(2, 3, 33, 64, 16) == 2 * 3 * 3 * 64 * 16 * 4
     assert rdm.rdm_ssm_saved_states_size(2, 3, 33, 64, 17) == 0
