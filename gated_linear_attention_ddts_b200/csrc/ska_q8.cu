@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) ska_q8_fill_kernel(const SkaQ8FillPa
 // before and behind the sweep of V, in which little is on its way: a kernel that only
 // streams the same V through the same rings takes 45 us, this one 83 (3.7 TB/s), of
 // which the tail's rows cost 13; the bf16 rings' kernel (ska.cu) takes 119 for 1.9
-// times the bytes.  One sequence, window 32768: 27 us, a second kernel joining 128
+// times the bytes.  One sequence, window 32768: 26 us, a second kernel joining 128
 // splits included.
 constexpr int kWarps = 8, kDecThreads = 32 * kWarps, kChunk = 512, kStride = kChunk + 4, kRing = 4;
 
@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
     auto& part = sm.part;
     auto& stat = sm.stat;
     const SkaQ8Cache& c = p.c;
+    chain_next();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, l4 = lane & 3;
     const int group = blockIdx.x % pl.groups, b = blockIdx.x / pl.groups, split = blockIdx.y;
     const int h0 = group * pl.G, nh = min(pl.G, c.H - h0);
@@ -820,6 +821,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
 constexpr int kJoinThreads = 256, kMostSplits = 128;
 template <int DV>
 __global__ void __launch_bounds__(kJoinThreads) ska_q8_join_kernel(const SkaQ8DecodeParams p, const Q8Plan pl) {
+    chain_wait();
     constexpr int ROWS = kJoinThreads / DV;
     __shared__ float f[kMostSplits], red[2][kJoinThreads / 32], part[ROWS][DV];
     const SkaQ8Cache& c = p.c;
@@ -865,6 +867,7 @@ __global__ void __launch_bounds__(kJoinThreads) ska_q8_join_kernel(const SkaQ8De
 }
 
 __global__ void ska_q8_advance_kernel(int* pos, int B) {
+    chain_wait();
     const int b = blockIdx.x * blockDim.x + threadIdx.x;
     if (b < B && pos[b] >= 0) pos[b] += 1;
 }
@@ -942,11 +945,9 @@ cudaError_t launch_decode_cfg(const SkaQ8DecodeParams& p, Q8Plan pl, cudaStream_
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, p, pl);
     if (e != cudaSuccess) return e;
     if (pl.splits > 1) {
-        ska_q8_join_kernel<DV><<<(unsigned)(p.c.B * p.c.H), kJoinThreads, 0, s>>>(p, pl);
-        e = cudaGetLastError();
+        e = launch_chained(ska_q8_join_kernel<DV>, dim3((unsigned)(p.c.B * p.c.H)), kJoinThreads, 0, s, p, pl);
     } else if (!pl.cluster && p.advance) {
-        ska_q8_advance_kernel<<<(p.c.B + 255) / 256, 256, 0, s>>>(p.c.pos, p.c.B);
-        e = cudaGetLastError();
+        e = launch_chained(ska_q8_advance_kernel, dim3((p.c.B + 255) / 256), 256, 0, s, p.c.pos, p.c.B);
     }
     return e;
 }

@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 2 
     constexpr int LPC = L::LPC, TH = L::THREADS, EW = kEw<CPB>, UNITS = (kTile / 4) * (CPB / 2);
     using Quad = typename Four<T>::Raw;
     using Raw = typename Pair<T>::Raw;
+    if (LOCAL) chain_next();
+    else chain_wait();
     extern __shared__ __align__(16) unsigned char smem_raw[];
     FwdSmem<T, N, CPB, LOCAL>& sm = *reinterpret_cast<FwdSmem<T, N, CPB, LOCAL>*>(smem_raw);
     auto &sD = sm.D, &sU = sm.U;
@@ -516,6 +518,7 @@ cudaError_t launch_fwd_pass(const SsmParams& p, const SegArgs& sg, cudaStream_t 
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)((long long)p.B * p.H * (p.D / CPB)), LOCAL ? sg.P - 1 : sg.P);
+    if (!LOCAL && sg.P > 1) return launch_chained(kern, grid, CPB * N / 4 + kEw<CPB>, smem, s, p, sg);
     kern<<<grid, CPB * N / 4 + kEw<CPB>, smem, s>>>(p, sg);
     return cudaGetLastError();
 }

@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
     using Quad = typename Four<T>::Raw;
     constexpr int LPC = L::LPC, TH = L::THREADS, EW = kEw<CPB>, UNITS = kQuads * (CPB / 2), WARPS = TH / 32, F = Red<N>::F;
     constexpr int CW = 32 / LPC;  // channels a warp
+    if (!LOCAL) chain_wait();
+    chain_next();
     extern __shared__ __align__(16) unsigned char smem_raw[];
     BwdSmem<T, N, CPB, LOCAL>& sm = *reinterpret_cast<BwdSmem<T, N, CPB, LOCAL>*>(smem_raw);
     const SsmParams& p = bp.f;
@@ -682,6 +684,7 @@ __global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 
 // weights' gradients and the edges, one value a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_finish_kernel(const SsmBwdParams bp, const BwdWork wk, const unsigned rowblocks) {
+    chain_wait();
     const SsmParams& p = bp.f;
     if (blockIdx.x < rowblocks) {
         const int per = p.N / 2;  // float4 of a row
@@ -817,6 +820,7 @@ cudaError_t launch_bwd_pass(const SsmBwdParams& bp, const BwdWork& wk, cudaStrea
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)((long long)bp.f.B * bp.f.H * wk.nblk), LOCAL ? wk.P - 1 : wk.P);
+    if (!LOCAL && wk.P > 1) return launch_chained(kern, grid, CPB * N / 4 + kEw<CPB>, smem, s, bp, wk);
     kern<<<grid, CPB * N / 4 + kEw<CPB>, smem, s>>>(bp, wk);
     return cudaGetLastError();
 }
@@ -844,8 +848,7 @@ cudaError_t launch_bwd_t(const SsmBwdParams& bp, const BwdWork& wk, cudaStream_t
     const unsigned rowblocks = (unsigned)(((size_t)p.B * p.G * p.T * (p.N / 2) + 255) / 256);
     const size_t hd = (size_t)p.H * p.D;
     const size_t n = hd * (p.N + kPar) + (wk.P > 1 && p.W > 1 ? (size_t)(wk.P - 1) * p.B * p.H * 3 * p.D : 0);
-    ssm_finish_kernel<T><<<rowblocks + (unsigned)((n + 255) / 256), 256, 0, s>>>(bp, wk, rowblocks);
-    return cudaGetLastError();
+    return launch_chained(ssm_finish_kernel<T>, dim3(rowblocks + (unsigned)((n + 255) / 256)), 256, 0, s, bp, wk, rowblocks);
 }
 
 }  // namespace

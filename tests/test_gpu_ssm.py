@@ -105,6 +105,16 @@ def test_segments(cuda_ok, dtype, T):
     ref.assert_near(y, yr, T + 16, "y without segments")
 
 
+@pytest.mark.parametrize("N", [16, 64])
+@pytest.mark.parametrize("T", [65, 130, 397, 1040])
+def test_segment_counts(cuda_ok, T, N):
+    """More segments than the chunks divide into (the last ones are empty), and
+    sequences that end a few tokens behind any 16th: the filter's gradient then
+    reaches over a cut to carried-out inputs of both sides."""
+    ends = [T, 1, 33, 34, 49, 50, 51, T // 32 * 16 + 1, T // 32 * 16 + 2]
+    check_all(ref.inputs(len(ends), 1, T, 16, N, seed=T + N), lengths=[min(n, T) for n in ends])
+
+
 def test_rows_behind_the_end_are_left(cuda_ok):
     i = ref.inputs(2, 2, 50, 32, 16, dtype=BF16, seed=11)
     d = cuda(i)
