@@ -546,10 +546,13 @@ template <typename T, int N>
 cudaError_t launch_step(const SsmStepParams& p, cudaStream_t s) {
     constexpr int CB = kStepThreads / (N / 4);
     const long long nblk = ((long long)p.H * p.D + CB - 1) / CB;
-    // Eight sequences a block where that leaves every SM eight blocks (one read of A
-    // for eight states, and 128 bytes a thread on their way), else one, so that the
-    // few blocks spread over the SMs.
-    const bool many = nblk * ((p.B + 7) / 8) >= 8LL * sm_count();
+    // Eight sequences a block (one read of A for eight states, 128 bytes a thread on
+    // their way) where blocks of one sequence would be more than the SMs hold at a
+    // time, about six each; fewer go out one by one and spread over the SMs.  Measured
+    // (us, one / eight): H16 D128 N64 of B4 3.15 / 3.19, B8 5.0 / 3.6, B32 11.6 / 7.0,
+    // B256 99.5 / 51.5; H24 D64 N16 of B16 3.0 / 4.0, B32 3.7 / 4.2, B48 5.1 / 4.2, B256
+    // 20.5 / 13.8.
+    const bool many = nblk * p.B > 6LL * sm_count();
     const long long grid = nblk * (many ? (p.B + 7) / 8 : p.B);
     if (many) ssm_step_kernel<T, N, 8><<<(unsigned)grid, kStepThreads, 0, s>>>(p);
     else ssm_step_kernel<T, N, 1><<<(unsigned)grid, kStepThreads, 0, s>>>(p);
