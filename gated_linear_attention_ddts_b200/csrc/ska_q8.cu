@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) ska_q8_fill_kernel(const SkaQ8FillPa
 // before and behind the sweep of V, in which little is on its way: a kernel that only
 // streams the same V through the same rings takes 45 us, this one 83 (3.7 TB/s), of
 // which the tail's rows cost 13; the bf16 rings' kernel (ska.cu) takes 119 for 1.9
-// times the bytes.  One sequence, window 32768: 26 us, a second kernel joining 128
+// times the bytes.  One sequence, window 32768: 24 us, a second kernel joining 74
 // splits included.
 constexpr int kWarps = 8, kDecThreads = 32 * kWarps, kChunk = 512, kStride = kChunk + 4, kRing = 4;
 
@@ -872,17 +872,24 @@ __global__ void ska_q8_advance_kernel(int* pos, int B) {
     if (b < B && pos[b] >= 0) pos[b] += 1;
 }
 
-// Heads of a group: as many as keep all eight warps busy (8, or fewer that leave
-// two, four or eight warps to each), the fewest groups among the best.
-int group_heads(int H) {
+// Heads of a group.  More heads share one read of the keys and make fewer CTAs, but
+// leave fewer warps to a head: a CTA of G heads takes about 9 + 3.9 G us for 512 slots
+// (G = 1 .. 8, d 128, two CTAs an SM), so the group is the one whose rounds of two CTAs
+// an SM cost least: the smallest that fits one round, large ones for large batches.
+// Measured (us, G = 1 / 2 / 4 / 8; H16 d128, * the choice): window 512 of B1 10.4* / 12.3 /
+// 16.0 / 23.9, B16 13.3* / 16.1 / 16.4 / 24.2, B32 25.3 / 17.7* / 19.8 / 29.0, B64 44.1 /
+// 33.4 / 25.1* / 29.3, B256 160 / 119 / 91 / 79*; window 32768 of B1 31.4 / 24.6 / 23.7* /
+// 25.7; window 4096 of B8 32.5 / 24.8 / 22.5* / 22.6.  B128 H12: 65.8 / 47.3 / 45.6, and
+// 37.8* with G = 6.
+int group_heads(int B, int H, int window) {
+    const long long round = 2LL * sm_count(), chunks = (window + kChunk - 1) / kChunk;
     int best = 1;
-    double most = 0.0;
-    for (int groups = (H + 7) / 8; groups <= H && groups <= (H + 7) / 8 + 8; ++groups) {
-        const int G = (H + groups - 1) / groups;
-        if ((H + G - 1) / G != groups) continue;
-        const double used = (double)H * (kWarps / G) / ((double)groups * kWarps);
-        if (used > most + 1e-9) {
-            most = used;
+    double least = 0.0;
+    for (int G = 1; G <= 8 && G <= H; ++G) {
+        const long long ctas = B * chunks * ((H + G - 1) / G);
+        const double cost = (double)((ctas + round - 1) / round) * (9.0 + 3.9 * G);
+        if (G == 1 || cost < least) {
+            least = cost;
             best = G;
         }
     }
@@ -891,12 +898,12 @@ int group_heads(int H) {
 
 Q8Plan plan(const SkaQ8DecodeParams& p) {
     Q8Plan pl;
-    pl.G = group_heads(p.c.H);
+    pl.G = group_heads(p.c.B, p.c.H, p.c.window);
     pl.groups = (p.c.H + pl.G - 1) / pl.G;
     const long long units = (long long)p.c.B * pl.groups;
     // two CTAs an SM; each split of at least 256 slots, in multiples of the largest block
     long long P = units > 0 ? 2LL * sm_count() / units : 1;
-    // short windows stay whole: a second launch and the join cost more than half a chunk
+    // windows of a chunk stay whole (10.4 us for B1 H16 window 512; 10.5 for window 1024 split in four)
     const long long most = p.c.window <= kChunk ? 1 : (p.c.window + 255) / 256;  // at most kMostSplits, the window at most 32768
     if (P > most) P = most;
     if (P < 1) P = 1;

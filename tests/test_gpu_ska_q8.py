@@ -100,6 +100,30 @@ def test_heads_and_positions(cuda_ok, kind, H):
     ref.assert_state(cache, caches, "after the last token")
 
 
+@pytest.mark.parametrize("B,H,d", [(296, 2, 64), (296, 3, 64), (296, 4, 64), (296, 5, 64), (296, 6, 64), (296, 7, 64), (296, 8, 64),
+                                   (148, 9, 64), (140, 11, 64), (148, 16, 64), (296, 8, 128)])
+def test_large_batches(cuda_ok, B, H, d):
+    """Batches so large that a block takes two to eight heads of a sequence, the last
+    group of a sequence fewer; sequences at every place of the ring."""
+    q, k, v = tokens(B, H, 44, d, d, seed=B + H)
+    lengths = [b % 40 + 1 for b in range(B)]
+    kind = KINDS[H % 2]
+    cache, caches = filled(k[:, :40], v[:, :, :40], 25, 16, kind, lengths)
+    for t in range(40, 44):
+        step(q[:, :, t], k[:, t], v[:, :, t], cache, caches, what=f"token {t}")
+    ref.assert_state(cache, caches, "after the last token")
+
+
+@pytest.mark.parametrize("B,H", [(10, 16), (20, 16), (40, 12)])
+def test_long_windows_of_batches(cuda_ok, B, H):
+    """Split windows with groups of two, four and more heads."""
+    q, k, v = tokens(B, H, 560, 64, 64, seed=B)
+    cache, caches = filled(k[:, :557], v[:, :, :557], 550, 64, KINDS[B // 10 % 2], [557 - 30 * (b % 9) for b in range(B)])
+    for t in range(557, 560):
+        step(q[:, :, t], k[:, t], v[:, :, t], cache, caches, what=f"token {t}")
+    ref.assert_state(cache, caches, "after the last token")
+
+
 @pytest.mark.parametrize("H", [65, 67, 72])
 def test_more_heads_than_a_cluster(cuda_ok, H):
     """More than eight groups of heads: the positions are advanced by a kernel of
