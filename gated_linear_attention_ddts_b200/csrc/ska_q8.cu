@@ -919,6 +919,13 @@ size_t plan_bytes(const SkaQ8DecodeParams& p, const Q8Plan& pl) {
     return pl.splits == 1 ? 0 : (size_t)p.c.B * p.c.H * pl.splits * (p.c.dv + 2) * 4;
 }
 
+// The groups of a sequence that run as one cluster, which advances the position itself;
+// beyond, a second kernel does (2 us of host time).  More than eight need the opt-in
+// size.  Measured (us, second kernel / cluster): 12 groups of B2 window 300 9.4 / 9.4, of
+// B20 window 512 13.1 / 13.5; 16 groups, which find room on the GPU less often, of B1
+// 10.4 / 10.4, of B8 10.5 / 13.1, of B16 13.1 / 21.5.
+constexpr int kMostCluster = 12;
+
 template <bool I8, int DK, int DV>
 cudaError_t launch_decode_cfg(const SkaQ8DecodeParams& p, Q8Plan pl, cudaStream_t s) {
     const size_t need = plan_bytes(p, pl);
@@ -932,7 +939,7 @@ cudaError_t launch_decode_cfg(const SkaQ8DecodeParams& p, Q8Plan pl, cudaStream_
         pl.m = pl.o + rows * DV;
         pl.l = pl.m + rows;
     }
-    pl.cluster = pl.splits == 1 && pl.groups <= 8;
+    pl.cluster = pl.splits == 1 && pl.groups <= kMostCluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)p.c.B * pl.groups), pl.splits);
     cfg.blockDim = dim3(kDecThreads);
@@ -949,6 +956,8 @@ cudaError_t launch_decode_cfg(const SkaQ8DecodeParams& p, Q8Plan pl, cudaStream_
     }
     auto kern = ska_q8_decode_kernel<I8, DK, DV>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e == cudaSuccess && pl.cluster && pl.groups > 8)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, p, pl);
     if (e != cudaSuccess) return e;
     if (pl.splits > 1) {
