@@ -256,8 +256,13 @@ __global__ void __launch_bounds__(kThreads) ska_q8_fill_kernel(const SkaQ8FillPa
 //   scores  16 slots a warp, mma (slots x d_k) (d_k x 8 heads), the shared key rows
 //           read once for the group's heads; into shared memory
 //   weights a warp (or 8 / heads of them) per head: running maxima and sum, then
-//           2^(s + log2 v_scale - m') as two f16 halves: the block's scale is part
-//           of the exponent, so blocks of any scale meet in one accumulator
+//           e = 2^(s + log2 v_scale - m' + 15) in f16, the rest of e times 2^11 in
+//           f16: the block's scale is part of the exponent, so blocks of any scale meet
+//           in one accumulator.  m' is the largest s + log2 v_scale, so e is at most
+//           2^15, f16's last power of two; its parts have 22 bits down to 2^-25 and
+//           end at 2^-36, 2^-51 of the heaviest.  (Two halves of a weight of at most 1
+//           end at 2^-24 both: 32767 tokens behind one of 16 nats more were 6% off.)
+//           A block of zeros counts for nothing, whatever its scale's exponent is.
 //   values  mma (d_v x 16 slots) (16 slots x the weight's halves), the codes turned
 //           into f16 pairs in registers (exact: e4m3 and int8 both fit f16's 11 bits)
 // Without the tensor cores the conversions and products of the values alone would
@@ -266,7 +271,10 @@ __global__ void __launch_bounds__(kThreads) ska_q8_fill_kernel(const SkaQ8FillPa
 // 1/256 of an mma a warp.  (Tried: mma on the codes themselves, e4m3 or int8, the
 // weights in four parts of that type: right to 2^-24, but more instructions in all,
 // 103 us against 85 at B256 H16 d128 window 512.)
-// The tail's slots go through the same steps in bf16, the weights in three parts.
+// The tail's slots are scored with the others; their values follow behind the sweep,
+// in bf16, under weights of at most 1 in three parts of bf16 (24 bits at any size): they
+// have no scale, so the sums of the cache are brought to the scores' own exponent first
+// and the tail has no say in m' (with a say in it, values of 1e-4 lost 6%).
 // Each warp's tiles (the keys', then the values' of its head) come through a ring
 // of its own, four tiles ahead (two or five measure the same).  Bound: the phases
 // before and behind the sweep of V, in which little is on its way: a kernel that only
@@ -280,10 +288,11 @@ template <int DK, int DV>
 struct Q8Smem {
     uint4 ring[kWarps][kRing][16 * (DK > DV ? DK : DV) / 16];
     float sc[kWarps][kStride];
+    float sct[kWarps][64];             // the tail's scores
     __half wt[kWarps][2][kChunk];
     __nv_bfloat16 qs[kWarps][DK + 8];  // rows 16 bytes off one another's banks
     float part[kWarps][DV];
-    float stat[kWarps][3];
+    float stat[kWarps][2];
     float lvs[kWarps][32];             // log2 of the chunk's value scales, by head and block
     float mx[kWarps][kWarps][2];       // a warp's largest scores by head, without and with the scales
     __half zero[16];
@@ -353,6 +362,38 @@ __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b
 __device__ __forceinline__ float finite_abs(float x) {
     const float a = fabsf(x);
     return a <= 3.4e38f ? a : 0.0f;  // neither infinite nor NaN (bf16 ends at 3.39e38)
+}
+
+// A block of zeros has the scale 1, which is no measure of anything: the exponent of its
+// value scale becomes -inf, so it neither lowers the weights of other blocks nor gets
+// one.  `one`: the lane's block (`rows` of them at `block`) has the scale 1, which some
+// other blocks have too, so their codes tell: the first 16 bytes, and if those are
+// zeros all of it, eight lanes a block.  (A head that is all zeros reads its codes twice
+// for it: B1 H16 d128 window 512 18 us instead of 11, B256 138 instead of 83.)
+template <bool I8, int DV>
+__device__ __noinline__ float without_zeros(const unsigned char* block, int rows, bool one, float exponent) {
+    constexpr unsigned ALL = 0xffffffffu;
+    constexpr uint32_t MAGNITUDE = I8 ? 0xffffffffu : 0x7f7f7f7fu;
+    const int lane = threadIdx.x & 31, part = lane >> 3;
+    const auto bits = [](const uint4& x) { return (x.x | x.y | x.z | x.w) & MAGNITUDE; };
+    unsigned left = __ballot_sync(ALL, one && bits(*reinterpret_cast<const uint4*>(block)) == 0);
+    while (left) {  // four blocks: part k of the warp has the k-th that is left
+        unsigned mine = left;
+        for (int k = 0; k < part; ++k) mine &= mine - 1;
+        const int src = mine ? __ffs(mine) - 1 : 0;
+        const uint4* q = reinterpret_cast<const uint4*>(__shfl_sync(ALL, reinterpret_cast<unsigned long long>(block), src));
+        const int n = __shfl_sync(ALL, rows, src) * (DV / 16);
+        uint32_t any = 0;
+        if (mine) {
+#pragma unroll 16
+            for (int i = lane & 7; i < n; i += 8) any |= bits(q[i]);
+        }
+        const unsigned full = __ballot_sync(ALL, any != 0);
+        const int at = __popc(left & ((1u << lane) - 1));
+        if ((left >> lane & 1) && at < 4 && (full >> 8 * at & 0xff) == 0) exponent = -INFINITY;
+        for (int k = 0; k < 4; ++k) left &= left - 1;
+    }
+    return exponent;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -452,7 +493,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
     __nv_bfloat16* kt = static_cast<__nv_bfloat16*>(c.k_tail) + (size_t)b * R * DK;
     __nv_bfloat16* vt = static_cast<__nv_bfloat16*>(c.v_tail) + bh0 * R * DV;
 
-    float m = -INFINITY, m2 = -3e38f, l = 0.0f;  // m of the scores, m2 with the scales in them
+    // m of the scores, m2 of the cache's with the scales in them, 15 less
+    float m = -INFINITY, m2 = -3e38f, l = 0.0f;
     float acc[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -558,7 +600,15 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
         for (int c0 = s0; c0 < s1; c0 += kChunk) {
             const int c1 = min(c0 + kChunk, s1);
             const float ksl = ks_next;
-            if (warp < nh) sm.lvs[warp][lane] = __log2f(vs_next);
+            if (warp < nh) {
+                // blocks of the chunk with a slot whose value comes from the codes
+                const int first = c0 + (lane << rs);
+                const bool one = vs_next == 1.0f && lane < kChunk >> rs && first < s1 && (first != at || pos >= w);
+                float e = __log2f(vs_next);
+                if (__any_sync(0xffffffffu, one))
+                    e = without_zeros<I8, DV>(c.v + ((bh0 + warp) * w + (one ? first : 0)) * DV, min(R, w - first), one, e);
+                sm.lvs[warp][lane] = e;
+            }
             if (c0 + kChunk < s1) fetch_scales(c0 + kChunk);
             __syncthreads();
             float cm[2] = {-INFINITY, -INFINITY}, cn[2] = {-3e38f, -3e38f};  // of heads 2 l4 and 2 l4 + 1
@@ -625,12 +675,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
                         const int i = t0 + g + 8 * r;
                         if (i > fill) continue;
                         const float a = s[2 * r] * (p.scale * kLog2e), e = s[2 * r + 1] * (p.scale * kLog2e);
-                        sc[2 * l4][at - c0 + i] = a;
-                        sc[2 * l4 + 1][at - c0 + i] = e;
+                        sc[2 * l4][at - c0 + i] = sm.sct[2 * l4][i] = a;
+                        sc[2 * l4 + 1][at - c0 + i] = sm.sct[2 * l4 + 1][i] = e;
                         cm[0] = fmaxf(cm[0], a);
                         cm[1] = fmaxf(cm[1], e);
-                        cn[0] = fmaxf(cn[0], a);
-                        cn[1] = fmaxf(cn[1], e);
                     }
                 }
 #pragma unroll
@@ -652,7 +700,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
 #pragma unroll
                 for (int k = 0; k < kWarps; ++k) {
                     nm = fmaxf(nm, sm.mx[k][hd][0]);
-                    nm2 = fmaxf(nm2, sm.mx[k][hd][1]);
+                    nm2 = fmaxf(nm2, sm.mx[k][hd][1] - 15.0f);
                 }
                 const float f2 = ex2_fast(m2 - nm2);
                 l *= m == nm ? 1.0f : ex2_fast(m - nm);
@@ -678,14 +726,15 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
                     }
                     const __half2 h0 = __floats2half2_rn(e[0], e[1]), h1 = __floats2half2_rn(e[2], e[3]);
                     const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-                    const __half2 r0 = __floats2half2_rn(e[0] - f0.x, e[1] - f0.y), r1 = __floats2half2_rn(e[2] - f1.x, e[3] - f1.y);
+                    const __half2 r0 = __floats2half2_rn((e[0] - f0.x) * 2048.0f, (e[1] - f0.y) * 2048.0f);
+                    const __half2 r1 = __floats2half2_rn((e[2] - f1.x) * 2048.0f, (e[3] - f1.y) * 2048.0f);
                     *reinterpret_cast<uint2*>(&wt[warp][0][i]) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
                     *reinterpret_cast<uint2*>(&wt[warp][1][i]) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&r0), *reinterpret_cast<const uint32_t*>(&r1));
                 }
                 __syncwarp();
-                // lanes g = 0 and 1 have the weights' halves, the others zeros
+                // lanes g = 0 and 1 have the weights' two parts, the others zeros
                 uint32_t wp = (uint32_t)__cvta_generic_to_shared(g < 2 ? &wt[warp][g][2 * l4] : &sm.zero[2 * l4]);
                 const uint32_t wstep = g < 2 ? 32 : 0;
                 // rows 2 l4 and 2 l4 + 1; 8 on lies 8 rows further
@@ -725,37 +774,49 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
                         mma_f16(acc[i], a, b0, b1);
                     }
                 }
-                if (tail_now)
-                    for (int t0 = 16 * sub; t0 <= fill; t0 += 16 * wph) {
-                        const __nv_bfloat16* row[4];
-                        float e[4];
+            }
+            if (c0 + kChunk < s1) __syncthreads();
+        }
+        if (busy) {
+            // From here on the sums are relative to m.  In two steps: the scales alone may be
+            // past float32's exponents.
+            const float f = ex2_fast(0.5f * (m2 - m)), f1 = f * 0x1p-11f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                acc[i][0] = acc[i][0] * f * f;
+                acc[i][1] = acc[i][1] * f1 * f;
+                acc[i][2] = acc[i][2] * f * f;
+                acc[i][3] = acc[i][3] * f1 * f;
+            }
+            if (tail_here)
+                for (int t0 = 16 * sub; t0 <= fill; t0 += 16 * wph) {
+                    const __nv_bfloat16* row[4];
+                    float e[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int i = t0 + 2 * l4 + (r & 1) + 4 * (r & 2), ic = min(i, fill);
+                        row[r] = (ic == fill ? vin + (size_t)hd * DV : vt + ((size_t)hd * R + ic) * DV) + VB * g;
+                        e[r] = i <= fill ? ex2_fast(sm.sct[hd][ic] - m) : 0.0f;
+                        for (int x = 0; x < g && x < 3; ++x) e[r] -= __bfloat162float(__float2bfloat16_rn(e[r]));
+                        if (g > 2) e[r] = 0.0f;
+                    }
+                    const uint32_t b0 = bf16_pair(e[0], e[1]), b1 = bf16_pair(e[2], e[3]);
+#pragma unroll
+                    for (int x = 0; x < VB / 8; ++x) {  // eight columns of the four rows at once
+                        uint32_t v[4][4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const int i = t0 + 2 * l4 + (r & 1) + 4 * (r & 2), ic = min(i, fill);
-                            row[r] = (ic == fill ? vin + (size_t)hd * DV : vt + ((size_t)hd * R + ic) * DV) + VB * g;
-                            e[r] = i <= fill ? ex2_fast(sc[hd][at - c0 + ic] - m2) : 0.0f;
-                            for (int x = 0; x < g && x < 3; ++x) e[r] -= __bfloat162float(__float2bfloat16_rn(e[r]));
-                            if (g > 2) e[r] = 0.0f;
+                            const uint4 q = *reinterpret_cast<const uint4*>(row[r] + 8 * x);
+                            v[r][0] = q.x; v[r][1] = q.y; v[r][2] = q.z; v[r][3] = q.w;
                         }
-                        const uint32_t b0 = bf16_pair(e[0], e[1]), b1 = bf16_pair(e[2], e[3]);
 #pragma unroll
-                        for (int x = 0; x < VB / 8; ++x) {  // eight columns of the four rows at once
-                            uint32_t v[4][4];
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const uint4 q = *reinterpret_cast<const uint4*>(row[r] + 8 * x);
-                                v[r][0] = q.x; v[r][1] = q.y; v[r][2] = q.z; v[r][3] = q.w;
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t a[4] = {__byte_perm(v[0][i], v[1][i], 0x5410), __byte_perm(v[0][i], v[1][i], 0x7632),
-                                                       __byte_perm(v[2][i], v[3][i], 0x5410), __byte_perm(v[2][i], v[3][i], 0x7632)};
-                                mma_bf16(acc[4 * x + i], a, b0, b1);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a[4] = {__byte_perm(v[0][i], v[1][i], 0x5410), __byte_perm(v[0][i], v[1][i], 0x7632),
+                                                   __byte_perm(v[2][i], v[3][i], 0x5410), __byte_perm(v[2][i], v[3][i], 0x7632)};
+                            mma_bf16(acc[4 * x + i], a, b0, b1);
                         }
                     }
-            }
-            __syncthreads();
+                }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // key tiles that no position needed
@@ -764,8 +825,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
         stat[warp][0] = m;
-        stat[warp][1] = m2;
-        stat[warp][2] = l;
+        stat[warp][1] = l;
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -785,9 +845,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
             float a = 0.0f, sum = 0.0f;
             for (int k = 0; k < wph; ++k) {
                 a += part[w0 + k][x];
-                sum += stat[w0 + k][2];
+                sum += stat[w0 + k][1];
             }
-            a *= ex2_fast(stat[w0][1] - stat[w0][0]);
             const size_t bh = bh0 + hh;
             if (pl.splits == 1) {
                 static_cast<__nv_bfloat16*>(p.o)[bh * DV + x] = __float2bfloat16_rn(a / sum);

@@ -437,8 +437,8 @@ rdm_status rdm_ska_decode(const rdm_ska_decode_args *args, rdm_stream_t stream);
  *     at least) with the block's largest magnitude within 448 * scale.
  *   RDM_CACHE_INT8: value = scale * code, scale the largest magnitude / 127,
  *     codes -127 .. 127 by rounding value / scale to nearest even.
- *   A block of zeros has the scale 1.  Keys and values are meant to be finite:
- *   others do not count for the scale; infinities take the largest code, NaN
+ *   A block of zeros has the scale 1 (by which decoding finds it, and leaves it
+ *   out).  Keys and values are meant to be finite: others do not count for the scale; infinities take the largest code, NaN
  *   stays NaN in e4m3 and becomes 0 in int8.  Decoding takes any positive scales.
  */
 typedef enum { RDM_CACHE_E4M3 = 0, RDM_CACHE_INT8 = 1 } rdm_cache_type;
@@ -473,6 +473,9 @@ rdm_status rdm_ska_q8_fill(const rdm_ska_q8_fill_args *args, rdm_stream_t stream
  * when advance_pos != 0.  A negative pos[b] leaves that sequence untouched and
  * makes rdm_ddts_sync_status return RDM_ERR_INVALID_ARG.  pos[b] must stay
  * below 2^31 - 1.
+ * Arithmetic is float32.  A cached token's softmax weight times the scale of its
+ * values enters with 22 bits where it is within 2^-40 of the head's largest such
+ * product, with fewer below, and as zero below 2^-51.
  *   workspace : optional scratch; with rdm_ska_q8_decode_workspace_size() bytes
  *               long windows of few sequences are split over several CTAs.
  *               Contents on entry are ignored; calls whose kernels may overlap
