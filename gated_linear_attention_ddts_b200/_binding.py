@@ -542,7 +542,8 @@ _packed = {}
 
 def _load_packed(name):
     """The library's function `name`, taking its arguments as packed bytes."""
-    if not _packed:
+    if not _packed:  # all of them are published at once: another thread may come in meanwhile
+        declared = {}
         lib = load()
         for layout, ty in ((_SSM, SsmArgs), (_SSM_BWD, SsmBwdArgs), (_SSM_STEP, SsmStepArgs), (_Q8_FILL, SkaQ8FillArgs),
                            (_Q8_DECODE, SkaQ8DecodeArgs)):
@@ -554,7 +555,8 @@ def _load_packed(name):
             size = n.endswith("_size")
             fn.argtypes = [ctypes.c_char_p] if size else [ctypes.c_char_p, _VP]
             fn.restype = ctypes.c_size_t if size else _I
-            _packed[n] = fn
+            declared[n] = fn
+        _packed.update(declared)
     return _packed[name]
 
 
