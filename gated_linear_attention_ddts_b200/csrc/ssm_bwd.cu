@@ -74,11 +74,14 @@ __device__ __forceinline__ void part_sync() {
     asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
 }
 
+// Blocks an SM for a block's scan threads: what their registers leave room for.
+constexpr int resident(int threads) { return threads > 128 ? 1 : threads > 64 ? 2 : 4; }
+
 // Scan warps and element-wise warps, a chunk apart as in the forward: while the
 // scan warps run chunk k (forward, then backwards), the others finish chunk k - 1
 // and make delta, u and p of chunk k + 1.
 template <typename T, int N, int CPB, bool LOCAL>
-__global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, CPB * N / 4 > 128 ? 1 : CPB * N / 4 > 64 ? 2 : 4)
+__global__ void __launch_bounds__(CPB * N / 4 + kEw<CPB>, resident(CPB * N / 4))
     ssm_bwd_kernel(const SsmBwdParams bp, const BwdWork wk) {
     using L = Lay<N, CPB>;
     using Raw = typename Pair<T>::Raw;
@@ -755,28 +758,33 @@ int channels_per_block(int D, int N) {
     return D < most ? D : most;
 }
 
-// Segments a sequence: the count of least cost, where two blocks an SM run at a time, a
-// segment costs its tokens and a chunk to start and end, and the first launch for the
-// states is a tenth of the work of all segments but one; each of at least two chunks.
+// Segments a sequence: the count of least cost, where a round is as many blocks as run at
+// a time, a segment costs its tokens and a chunk to start and end, and the first launch for
+// the states is a tenth of the work of all segments but one; each of at least two chunks,
+// and whole sequences unless a cut saves 3% by this count.
 // Measured, a training step with D64 N16 bf16 (us, whole sequences / this rule's P):
-// B1 H24 T4096 871 / 324 (6), B2 H24 T4096 958 / 625 (3), B4 H24 T2048 664 / 563 (3),
-// B1 H3 T4096 787 / 73 (49), B1 H4 T512 113 / 31 (16), B3 H20 T2048 505 / 388 (7); it
-// keeps P = 1 at B16 H24 T512, 514 against 549 of P = 3, and at B32 H24 T128, 268
-// against 336.  At B5 H24 T777 it loses: 301 (6) against 278.
+// B1 H24 T4096 857 / 321 (6), B2 H24 T4096 947 / 616 (3), B4 H24 T2048 653 / 554 (3),
+// B1 H3 T4096 769 / 72 (49), B1 H4 T512 110 / 29 (16), B3 H20 T2048 499 / 383 (7); it
+// keeps P = 1 at B16 H24 T512, 507 against 547 of P = 3, at B32 H24 T128, 266 against
+// 330, and at B5 H24 T777, 273 against 298 of P = 6.  Four blocks an SM, B2 H24 T2048
+// D16 N16: 386 / 104 (12; 153 with the 6 that two an SM would ask for).  One, N128 T2048:
+// B2 H8 D64 791 (1) against 869 of P = 3, B1 H4 D16 561 / 75 (18).
 int segments(const SsmParams& p) {
-    const long long blocks = (long long)p.B * p.H * (p.D / channels_per_block(p.D, p.N)), round = 2LL * sm_count();
+    const int cpb = channels_per_block(p.D, p.N);
+    const long long blocks = (long long)p.B * p.H * (p.D / cpb), round = (long long)resident(cpb * p.N / 4) * sm_count();
     const int most = p.T / (2 * kSsmChunk) < 64 ? p.T / (2 * kSsmChunk) : 64;
     int best = 1;
-    double least = 0;
+    double whole = 0, least = 0;
     for (int P = 1; P == 1 || P <= most; ++P) {
         const long long rounds = (blocks * P + round - 1) / round;
         const double cost = rounds * ((double)p.T / P + kSsmChunk) * (1.0 + 0.1 * (P - 1) / P);
+        if (P == 1) whole = cost;
         if (P == 1 || cost < least) {
             least = cost;
             best = P;
         }
     }
-    return best;
+    return least < 0.97 * whole ? best : 1;
 }
 
 size_t up(size_t n) { return (n + 63) / 64 * 64; }  // floats, so that each part starts on 256 bytes
