@@ -484,6 +484,10 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmStepPar
 // blocks an SM, each segment of at least two tiles.  Whole sequences of at most two
 // blocks an SM run 16 channels a block (B4: 132 us); with more, 32 is faster
 // (B8 T2048: 213 against 245).
+// N = 128 (256 scan threads a block, two blocks an SM) keeps them whole from three
+// quarters of the SMs on: B1 D64 T4096 whole / cut, 64 blocks 322 / 198, 104 blocks
+// 323 / 292, 112 blocks 323 / 331, 128 blocks 323 / 386, 144 blocks 323 / 387.  The others
+// at 128 blocks, T4096: N64 233 / 206, N32 219 / 210, N16 207 / 225 (f32 238 / 231).
 struct Cut {
     int cpb, P;
 };
@@ -493,7 +497,7 @@ Cut cut(const SsmParams& p) {
     if (c.cpb > p.D) c.cpb = p.D;
     const long long blocks = (long long)p.B * p.H * (p.D / c.cpb), sms = sm_count();
     c.P = 1;
-    if (blocks >= sms) {
+    if (blocks >= (p.N == 128 ? sms * 3 / 4 : sms)) {
         if (p.N == 16 && blocks < 2 * sms) c.cpb = 16;
         return c;
     }
