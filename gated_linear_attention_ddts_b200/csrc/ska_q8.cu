@@ -259,11 +259,11 @@ __global__ void __launch_bounds__(kThreads) ska_q8_fill_kernel(const SkaQ8FillPa
 //           e = 2^(s + log2 v_scale - m' + 15) in f16, the rest of e times 2^11 in
 //           f16: the block's scale is part of the exponent, so blocks of any scale meet
 //           in one accumulator.  m' is the largest s + log2 v_scale, so e is at most
-//           2^15, f16's last power of two; its parts have 22 bits down to 2^-25 and
-//           end at 2^-36, 2^-51 of the heaviest.  (Two halves of a weight of at most 1
-//           end at 2^-24 both: 32767 tokens behind one of 16 nats more were 6% off.)
-//           A block of zeros counts for nothing, whatever its scale's exponent is.
-//   values  mma (d_v x 16 slots) (16 slots x the weight's halves), the codes turned
+//           2^15, f16's last power of two; its parts have 22 bits down to 2^-14, fewer
+//           below, and end at 2^-36, 2^-51 of the heaviest.  (Two halves of a weight of
+//           at most 1 end at 2^-24 both: 32767 tokens behind one of 16 nats more, whose
+//           value was zero, came out 6% off.)  Blocks of zeros count for nothing.
+//   values  mma (d_v x 16 slots) (16 slots x the weights' two parts), the codes turned
 //           into f16 pairs in registers (exact: e4m3 and int8 both fit f16's 11 bits)
 // Without the tensor cores the conversions and products of the values alone would
 // cost about 70 of an SM's 128 lane operations a clock at the memory's rate; with
@@ -274,14 +274,15 @@ __global__ void __launch_bounds__(kThreads) ska_q8_fill_kernel(const SkaQ8FillPa
 // The tail's slots are scored with the others; their values follow behind the sweep,
 // in bf16, under weights of at most 1 in three parts of bf16 (24 bits at any size): they
 // have no scale, so the sums of the cache are brought to the scores' own exponent first
-// and the tail has no say in m' (with a say in it, values of 1e-4 lost 6%).
+// and the tail has no say in m' (with a say in it, values of 1e-4 lost 5%).
 // Each warp's tiles (the keys', then the values' of its head) come through a ring
 // of its own, four tiles ahead (two or five measure the same).  Bound: the phases
 // before and behind the sweep of V, in which little is on its way: a kernel that only
-// streams the same V through the same rings takes 45 us, this one 83 (3.7 TB/s), of
+// streams the same V through the same rings takes 45 us, this one 82 (3.7 TB/s), of
 // which the tail's rows cost 13; the bf16 rings' kernel (ska.cu) takes 119 for 1.9
-// times the bytes.  One sequence, window 32768: 24 us, a second kernel joining 74
-// splits included.
+// times the bytes.  One sequence, window 32768: 25 us, a second kernel joining 74
+// splits included.  Registers are at the limit of two CTAs an SM (128); 16 bytes spill at
+// d_k = d_v = 128, 32 at 64, none at the others.
 constexpr int kWarps = 8, kDecThreads = 32 * kWarps, kChunk = 512, kStride = kChunk + 4, kRing = 4;
 
 template <int DK, int DV>
@@ -820,7 +821,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) ska_q8_decode_kernel(const Ska
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // key tiles that no position needed
-    // ---- join the halves and parts, then the warps of a head
+    // ---- join the parts of the weights, then the warps of a head
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
@@ -939,7 +940,10 @@ __global__ void ska_q8_advance_kernel(int* pos, int B) {
 // 16.0 / 23.9, B16 13.3* / 16.1 / 16.4 / 24.2, B32 25.3 / 17.7* / 19.8 / 29.0, B64 44.1 /
 // 33.4 / 25.1* / 29.3, B256 160 / 119 / 91 / 79*; window 32768 of B1 31.4 / 24.6 / 23.7* /
 // 25.7; window 4096 of B8 32.5 / 24.8 / 22.5* / 22.6.  B128 H12: 65.8 / 47.3 / 45.6, and
-// 37.8* with G = 6.
+// 37.8* with G = 6.  The cost was fitted at d 128 and 512 slots; at d 64 the choice is
+// within 6% of the best of G = 1, 2, 3, 4, 6, 8 for windows of 20 (B1 H12 7.5 against 7.3, B32 H16
+// 9.7 / 9.2, B128 H16 14.6, B256 H12 22.0), 64 (B256 H24 43.5), 128 (B256 H12 33.6), 512 (B1 9.2, B32 13.4
+// against 13.1, B128 H12 31.0, B256 H16 56.0), 4096 (B8 H16 19.4) and 32768 (B1 18.7).
 int group_heads(int B, int H, int window) {
     const long long round = 2LL * sm_count(), chunks = (window + kChunk - 1) / kChunk;
     int best = 1;
@@ -979,10 +983,11 @@ size_t plan_bytes(const SkaQ8DecodeParams& p, const Q8Plan& pl) {
 }
 
 // The groups of a sequence that run as one cluster, which advances the position itself;
-// beyond, a second kernel does (2 us of host time).  More than eight need the opt-in
-// size.  Measured (us, second kernel / cluster): 12 groups of B2 window 300 9.4 / 9.4, of
-// B20 window 512 13.1 / 13.5; 16 groups, which find room on the GPU less often, of B1
-// 10.4 / 10.4, of B8 10.5 / 13.1, of B16 13.1 / 21.5.
+// beyond, a second kernel does.  More than eight need the opt-in size.  Measured (us on
+// the GPU, second kernel / cluster): 12 groups of B2 window 300 9.4 / 9.4, of B20 window
+// 512 13.1 / 13.5: what a cluster of twelve saves is the second launch's 2 us of host time
+// in calls that the host bounds.  16 groups find room on the GPU less often: of B1
+// 10.4 / 10.4, of B8 10.5 / 13.1, of B16 13.1 / 21.5.  (Between 12 and 16: not measured.)
 constexpr int kMostCluster = 12;
 
 template <bool I8, int DK, int DV>

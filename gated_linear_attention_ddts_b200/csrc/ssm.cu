@@ -555,7 +555,8 @@ cudaError_t launch_step(const SsmStepParams& p, cudaStream_t s) {
     // time, about six each; fewer go out one by one and spread over the SMs.  Measured
     // (us, one / eight): H16 D128 N64 of B4 3.15 / 3.19, B8 5.0 / 3.6, B32 11.6 / 7.0,
     // B256 99.5 / 51.5; H24 D64 N16 of B16 3.0 / 4.0, B32 3.7 / 4.2, B48 5.1 / 4.2, B256
-    // 20.5 / 13.8.
+    // 20.5 / 13.8; H32 D128 N128, groups of eight not full, B2 5.5 / 5.2, B3 6.3 / 5.4, B5
+    // 8.9 / 5.5, B9 15.0 / 9.5, B17 32.4 / 21.2.
     const bool many = nblk * p.B > 6LL * sm_count();
     const long long grid = nblk * (many ? (p.B + 7) / 8 : p.B);
     if (many) ssm_step_kernel<T, N, 8><<<(unsigned)grid, kStepThreads, 0, s>>>(p);

@@ -19,10 +19,10 @@
 // are cut into segments as in the forward; a first launch then runs G alone over
 // each segment but the first from zero, and each block folds the segments behind its
 // own.  The convolution's reach over a segment's end is added by the last kernel.
-// Bound: instructions (147 a warp, token and 128 states, 54% of the issue slots) and
-// the shared-memory pipe (40%); the exponentials, the floor, are 26%.  B4 H24 T2048
-// D64 N16 bf16: forward and backward 560 us, 361 of them this kernel
-// and 68 its first launch.
+// Bound: instructions (145 a warp, token and 128 states, 54% of the issue slots) and
+// the shared-memory pipe (41%); the exponentials, the floor, are 27%.  B4 H24 T2048
+// D64 N16 bf16: forward and backward 554 us.  float32 is at the limit of the registers
+// from N = 32 on: 12 to 16 bytes spill there, none elsewhere.
 #include "launch.h"
 #include "ssm_common.cuh"
 

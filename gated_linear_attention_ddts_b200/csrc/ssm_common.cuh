@@ -36,8 +36,10 @@ __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
 // on average where decays lie (measured on the card: 0.5 to 2.6e-8 for exponents
 // from -0.001 to -1), which a long memory adds up token by token (dA of 2048 tokens
 // 1.8e-6 off, against 1.0e-6 for float32 with a correctly rounded exponential); an
-// exponent larger by as much costs nothing in the same multiply-add (0.8e-6).  A
-// step of zero still gives 1.
+// exponent larger by as much costs nothing in the same multiply-add (0.8e-6).  It is
+// the mean of exponents between -1 and 0; below -1 it is less than half a step of the
+// exponent itself, and decays forget soon enough for neither to matter.  The folds
+// over whole segments go without.  A step of zero still gives 1.
 __device__ __forceinline__ float2 decay2(float2 delta, float2 A2) { return ex22(fma2(delta, A2, two(2.5e-8f))); }
 
 // softplus(x) = max(x, 0) + log1p(e^-|x|).  The steps sit near 1e-3..1e-1, where

@@ -431,15 +431,16 @@ rdm_status rdm_ska_decode(const rdm_ska_decode_args *args, rdm_stream_t stream);
  * from there, and rounded once when the block is full; slots of that block that
  * the tail has not reached still hold the round before.  So every token is
  * rounded at most once, and a prompt leaves the same cache as its tokens one by
- * one.  Slots never written are never read.
+ * one.  What slots never written hold is not used.
  *
  *   RDM_CACHE_E4M3: value = scale * code, scale the least power of two (2^-126
  *     at least) with the block's largest magnitude within 448 * scale.
  *   RDM_CACHE_INT8: value = scale * code, scale the largest magnitude / 127,
  *     codes -127 .. 127 by rounding value / scale to nearest even.
  *   A block of zeros has the scale 1 (by which decoding finds it, and leaves it
- *   out).  Keys and values are meant to be finite: others do not count for the scale; infinities take the largest code, NaN
- *   stays NaN in e4m3 and becomes 0 in int8.  Decoding takes any positive scales.
+ *   out).  Keys and values are meant to be finite: others do not count for the
+ *   scale; infinities take the largest code, NaN stays NaN in e4m3 and becomes 0
+ *   in int8.  Decoding takes any positive scales.
  */
 typedef enum { RDM_CACHE_E4M3 = 0, RDM_CACHE_INT8 = 1 } rdm_cache_type;
 
@@ -474,7 +475,7 @@ rdm_status rdm_ska_q8_fill(const rdm_ska_q8_fill_args *args, rdm_stream_t stream
  * makes rdm_ddts_sync_status return RDM_ERR_INVALID_ARG.  pos[b] must stay
  * below 2^31 - 1.
  * Arithmetic is float32.  A cached token's softmax weight times the scale of its
- * values enters with 22 bits where it is within 2^-40 of the head's largest such
+ * values enters with 22 bits where it is within 2^-29 of the head's largest such
  * product, with fewer below, and as zero below 2^-51.
  *   workspace : optional scratch; with rdm_ska_q8_decode_workspace_size() bytes
  *               long windows of few sequences are split over several CTAs.

@@ -54,7 +54,7 @@ def check(c, q, k, v, scale, what, **kw):
     p = torch.softmax(q.double() @ held[0].t() * scale, -1)
     want = torch.stack([p[h] @ held[1 + h] for h in range(c.H)])
     mean = torch.stack([p[h] @ held[1 + h].abs() for h in range(c.H)])
-    heavy = torch.stack([(p[h] * blocks[h].repeat_interleave(c.R)[:c.w]).max() for h in range(c.H)])
+    heavy = torch.stack([(p[h] * blocks[h].repeat_interleave(c.R)[:p.shape[1]]).max() for h in range(c.H)])
     bound = 2.0 ** -8 * want.abs() + 2.0 ** -15 * mean + c.w * 2.0 ** -50 * heavy[:, None]
     assert torch.isfinite(o).all(), what
     worst = ((o - want).abs() / bound.clamp(min=1e-300)).max().item()
@@ -161,3 +161,35 @@ def test_scales_that_rise_and_fall_over_the_window(cuda_ok, kind, slot, falling)
     q[:, 0] = 2.0
     v = normal(24, 2, 64) * 1e-10
     check(resident(K, V, 2 * w + slot, 64, kind), q, normal(23, 64), v, 1.0, f"slot {slot}", workspace=False)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,kw", WINDOWS)
+@pytest.mark.parametrize("half", [False, True])
+def test_blocks_whose_scale_is_one(cuda_ok, kind, window, kw, half):
+    """Blocks that begin with zeros and have the scale 1 for their largest value's
+    sake, beside blocks of zeros or not."""
+    V = normal(25, 2, window, 128).clamp(-3, 3)
+    V[:, ::64, :64] = 0
+    V[:, 5::64, 77] = 127.0 if kind == torch.int8 else 448.0
+    if half:
+        V[:, :window // 128 * 64] = 0
+    c = resident(normal(26, window, 64), V, window + 90, 64, kind)
+    assert c.scale[1][:window // 64].eq(1).all()
+    check(c, normal(27, 2, 64), normal(28, 64), normal(29, 2, 128), 1 / 8, "scale 1", **kw)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tokens", [1, 40, 64, 700])
+@pytest.mark.parametrize("sigma", [1e-4, 1e-20])
+def test_small_values_in_the_first_round(cuda_ok, kind, tokens, sigma):
+    """Slots behind the last token hold codes of a large scale or zeros with the scale
+    1; neither counts."""
+    K, V = normal(30, 1000, 64), normal(31, 2, 1000, 64) * sigma
+    V[:, 320:384] = 0
+    c = ref.Cache(2, 64, 64, 1000, 64, kind)
+    for t in range(tokens):
+        c.add(K[t], V[:, t])
+    for h in (1, 2):
+        c.codes[h][-200:], c.scale[h][-3:] = 100.0 if kind == torch.int8 else 240.0, 2.0 ** 20
+    check(c, normal(32, 2, 64), normal(33, 64), normal(34, 2, 64) * sigma, 1 / 8, f"{tokens} tokens")
